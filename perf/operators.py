@@ -14,7 +14,7 @@ library's calls (`own`):
             per sequence over the 4-bit pages
 
 The 4-bit pool is uint8 [num_blocks][kv_heads][1088 * d / 64]: per (block, KV
-head) one record of K codes, V codes, K scales, V scales for 16 tokens.  A
+head) one record of K codes, V codes and scales for 16 tokens.  A
 code is E2M1 (sign, two exponent bits, one mantissa bit: 0, .5, 1, 1.5, 2, 3,
 4, 6); each token has one bf16 scale per 64 head dims.  Byte positions inside
 a record are those of `record_layout`.
@@ -117,18 +117,18 @@ def record_bytes(d):
 def record_layout(d, device):
     """Byte offsets in a record: K codes [16, d/2] (low nibble: the even dim),
     V codes [16, d/2] (the same), and the first bytes of the K and V scales
-    [16, d/64].  K: rows 4c + 2n + j sit with column 2c + j of fragment n, d/4
-    consecutive dims to a lane.  V: a token's 8 consecutive dims are one
-    32-bit word, the words of four consecutive tokens one 16-byte chunk."""
+    [16, d/64].  Codes lie in planes of 512 bytes, one per 64 dims.  K: token
+    4c + 2n + j sits with column 2c + j of fragment n, 16 consecutive dims to
+    a lane.  V: a token's 8 consecutive dims are one 32-bit word, the words of
+    four consecutive tokens one 16-byte chunk.  Scales: per 64 dims and four
+    consecutive tokens a chunk of their four K and four V scales."""
     r = torch.arange(BLOCK)[:, None]
     e = 2 * torch.arange(d // 2)[None, :]
     col, n = 2 * (r // 4) + (r & 1), (r // 2) & 1
-    lane = 4 * col + e // (d // 4)
-    b = (e % (d // 4)) // 2
-    k = lane * 16 + n * 8 + b if d == 64 else n * 512 + lane * 16 + b
+    k = (e // 64) * 512 + (4 * col + (e % 64) // 16) * 16 + n * 8 + (e % 16) // 2
     v = 8 * d + (e // 64) * 512 + (((e % 64) // 8) * 4 + r // 4) * 16 + (r & 3) * 4 + (e % 8) // 2
-    s = 16 * d + 2 * (torch.arange(d // GROUP)[None, :] * BLOCK + r)
-    return k.to(device), v.to(device), s.to(device), (s + 2 * BLOCK * (d // GROUP)).to(device)
+    s = 16 * d + 64 * torch.arange(d // GROUP)[None, :] + 16 * (r // 4) + 2 * (r % 4)
+    return k.to(device), v.to(device), s.to(device), (s + 8).to(device)
 
 
 @functools.lru_cache(maxsize=None)
@@ -422,13 +422,12 @@ def _values64(rec, d, which):
     r = torch.arange(BLOCK, device=rec.device)[:, None]
     e = torch.arange(d, device=rec.device)[None, :]
     if which == 0:
-        wide = d // 4
-        lane = (2 * (r // 4) + r % 2) * 4 + e // wide
-        byte = (lane * 16 + (r // 2 % 2) * (8 if d == 64 else 512) + e % wide // 2)
+        lane = (2 * (r // 4) + r % 2) * 4 + e % 64 // 16
+        byte = e // 64 * 512 + lane * 16 + (r // 2 % 2) * 8 + e % 16 // 2
     else:
         byte = 8 * d + e // 64 * 512 + ((e % 64 // 8) * 4 + r // 4) * 16 + r % 4 * 4 + e % 8 // 2
     code = (rec[..., byte].long() >> (4 * (e % 2))) & 15
-    at = 16 * d + which * 32 * (d // 64) + 2 * (e // 64 * BLOCK + r)
+    at = 16 * d + e // 64 * 64 + r // 4 * 16 + which * 8 + r % 4 * 2
     bits = rec[..., at].int() | (rec[..., at + 1].int() << 8)
     scale = (bits << 16).view(torch.float32).double()
     ex, man = (code >> 1) & 3, (code & 1).double()
