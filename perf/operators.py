@@ -142,12 +142,14 @@ def byte_values(device):
 
 def quantise(x):
     """Codes and bf16 scales of x [..., d]: per 64 dims, scale = bf16(max|x| / 6),
-    code = the nearest E2M1 of x / scale, halves to the even code."""
+    code = the nearest E2M1 of x / scale, halves to the even code (|x| against
+    the midpoints times the scale, products that 32 bits hold exactly)."""
     g = x.float().unflatten(-1, (-1, GROUP))
     scale = (g.abs().amax(-1) / 6).to(torch.bfloat16)
-    q = torch.where(scale[..., None] > 0, g.abs() / scale[..., None].float(), 0.0)
-    code = ((q > 0.25).to(torch.uint8) + (q >= 0.75) + (q > 1.25) + (q >= 1.75) + (q > 2.5)
-            + (q >= 3.5) + (q > 5.0))
+    m, s = g.abs(), scale[..., None].float()
+    code = ((m > 0.25 * s).to(torch.uint8) + ((m >= 0.75 * s) & (m > 0)) + (m > 1.25 * s)
+            + ((m >= 1.75 * s) & (m > 0)) + (m > 2.5 * s) + ((m >= 3.5 * s) & (m > 0)) + (m > 5.0 * s))
+    code = torch.where(s > 0, code, 0).to(torch.uint8)
     code = torch.where(g < 0, code + 8, code).to(torch.uint8).flatten(-2)
     return code[..., 0::2] | (code[..., 1::2] << 4), scale
 
