@@ -30,9 +30,10 @@
  *   start while this library's preceding kernel on the stream is still
  *   running and read the batch's metadata (context lengths, block tables,
  *   prefill positions and token rows) early, before it waits for that kernel
- *   and touches anything else.  No kernel of the library writes that
- *   metadata, and any other kernel on the stream completes before the next
- *   one of the library starts, so stream order holds for every input.
+ *   and touches anything else.  The one kernel of the library that writes
+ *   that metadata (photon_build_step_metadata_device) lets nothing start
+ *   before its end, and any other kernel on the stream completes before the
+ *   next one of the library starts, so stream order holds for every input.
  * Errors.  Every call returns a photon_status.  Arguments the host can check
  *   are checked before anything is launched (PHOTON_ERR_INVALID_ARG /
  *   PHOTON_ERR_UNSUPPORTED / PHOTON_ERR_WORKSPACE); a failed launch returns
@@ -85,6 +86,7 @@ typedef enum {
 #define PHOTON_DEVERR_BLOCK_RANGE 0x2u   /* a block_tables entry outside [0, num_blocks): page skipped */
 #define PHOTON_DEVERR_CONTEXT_RANGE 0x4u /* a context length above max_context_len or the table width: clamped */
 #define PHOTON_DEVERR_WAIT_TIMEOUT 0x8u  /* a bounded wait on a page copy gave up: item abandoned */
+#define PHOTON_DEVERR_METADATA 0x10u     /* photon_build_step_metadata_device refused a step (totals[3]) */
 
 /* Human-readable name of a status value (static string, never NULL). */
 const char *photon_status_string(int status);
@@ -372,6 +374,74 @@ int photon_paged_attention_partial_fp8(const void *q, const void *k_cache, const
                                        void *workspace, size_t workspace_bytes,
                                        photon_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit KV cache: E2M1 codes (sign, two exponent bits, one mantissa bit:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one bf16 scale per token, KV head and 64
+ * head dims, computed at the write: 4.25 bits per value, no calibration.
+ *
+ * Layout: one pool for K and V, uint8 [num_blocks][num_kv_heads][record],
+ * record = photon_kv_cache_fp4_record_bytes(head_dim) = 17 * head_dim bytes
+ * for the 16 tokens of a block, head_dim 64 or 128.  Inside a record the codes
+ * lie in the order of the attention kernel's fragments (csrc/fp4.cuh gives
+ * every byte); no byte belongs to two tokens.  value = code * scale.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of one (block, KV head) record; 0 for a head_dim without one. */
+size_t photon_kv_cache_fp4_record_bytes(int32_t head_dim);
+
+/*
+ * photon_kv_cache_write_fp4 -- the batched RoPE-fused write into a 4-bit pool.
+ * For every token with slot >= 0 and every KV head, y = RoPE(k) (v as it is)
+ * rounded once to in_dtype, the value photon_kv_cache_write would store; per
+ * 64 dims
+ *   scale = bf16(max |y| / 6)   (the fp32 quotient, both to nearest-even)
+ *   code  = nearest E2M1 of y / scale, halves to the even code, |code| <= 6
+ * A group of zeros has scale 0; one that holds an infinity or a NaN has a NaN
+ * scale and reads back as NaN.
+ *   k, v      device [num_tokens][num_kv_heads][head_dim], in_dtype (f32 or bf16), 16-B aligned
+ *   kv_cache  device 4-bit pool, 16-B aligned
+ * head_dim 64 or 128 (PHOTON_ERR_UNSUPPORTED otherwise).  Other arguments and
+ * errors as photon_kv_cache_write.
+ */
+int photon_kv_cache_write_fp4(const void *k, const void *v, const int32_t *positions,
+                              const int64_t *slot_mapping, void *kv_cache, int32_t num_tokens,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                              int64_t num_blocks, photon_dtype in_dtype, float rope_theta,
+                              photon_rope rope_style, photon_stream_t stream);
+
+/*
+ * photon_kv_cache_read_fp4 -- the cached rows of the tokens at slot_mapping,
+ * code * scale rounded once to out_dtype: a prefix held in 4 bits that a
+ * bf16 prefill attends to, or a cache moved to another type.  K comes back
+ * rotated, as written.
+ *   slot_mapping  device int64 [num_tokens], any order, repeats allowed; a
+ *                 token with slot -1 leaves its rows of k and v as they were,
+ *                 one outside the pool too (PHOTON_DEVERR_SLOT_RANGE)
+ *   k, v          device [num_tokens][num_kv_heads][head_dim], out_dtype (f32
+ *                 or bf16), 16-B aligned (outputs)
+ */
+int photon_kv_cache_read_fp4(const void *kv_cache, const int64_t *slot_mapping, void *k, void *v,
+                             int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int64_t num_blocks, photon_dtype out_dtype,
+                             photon_stream_t stream);
+
+/*
+ * photon_paged_attention_decode_fp4 -- photon_paged_attention_decode over a
+ * 4-bit pool: the same attention on the dequantised values.  q is bf16
+ * (already rotated) of any magnitude.  The scores, softmax and sums are fp32;
+ * a softmax weight times its V scale enters the second product in f16 (11
+ * significant bits) for a bf16 output, as f16 and its f16 remainder (22) for
+ * an fp32 one.  Workspace as for photon_paged_attention_decode; the split-K
+ * pieces are equal runs of pages as in photon_paged_attention_decode_fp8.
+ */
+int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const int32_t *block_tables,
+                                      const int32_t *context_lens, float scale, void *out,
+                                      int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                      int32_t max_blocks_per_seq, int32_t max_context_len,
+                                      int32_t partition_size, photon_dtype out_dtype, void *workspace,
+                                      size_t workspace_bytes, photon_stream_t stream);
+
 /*
  * Reads (and, if clear != 0, resets) the sticky PHOTON_DEVERR_* bits of the
  * current device.  Synchronises the device: a diagnostic, not a hot-path call.
@@ -450,6 +520,47 @@ int photon_build_step_metadata(int32_t num_seqs, const int32_t *num_computed_tok
                                photon_block_pool *pool, int32_t max_tokens, int32_t *token_seq,
                                int32_t *positions, int64_t *slot_mapping, int32_t *context_lens,
                                int32_t *num_tokens_out, int32_t *max_context_len_out);
+
+/*
+ * photon_build_step_metadata_device -- photon_build_step_metadata on the GPU:
+ * one kernel on `stream`, from request lengths and a pool of free blocks that
+ * live in device memory, so that a step (and a captured graph of it) needs no
+ * copy from the host.  All arrays are DEVICE memory.
+ *
+ * Sequence s holds ceil(num_computed_tokens[s] / 16) blocks, the first entries
+ * of its block_tables row, and
+ *   num_new_tokens[s] >= 0  writes that many tokens: its row grows to cover
+ *                           them (0: an idle row, unchanged), context_lens[s]
+ *                           = num_computed_tokens[s] + num_new_tokens[s];
+ *   num_new_tokens[s] < 0   is released: its blocks return to the pool, their
+ *                           row entries become -1, context_lens[s] = 0.
+ * The pool is a stack, free_blocks[0 .. num_free - 1], its last entry handed
+ * out first.  Released blocks are pushed first, in order of sequence and row;
+ * then blocks are taken in order of sequence and row -- what
+ * photon_block_pool_free and photon_build_step_metadata would do.
+ *   free_blocks   int32 [num_blocks] (in/out; entries past num_free are written by releases)
+ *   num_free      int32 [1]; num_free_out int32 [1], may be the same address
+ *   token_seq, positions, slot_mapping  [max_tokens] outputs; entries past the
+ *                 step's tokens are 0, -1 and -1: the cache writes skip such a
+ *                 token, a prefill gives it a zero row
+ *   context_lens  int32 [num_seqs] output (not overlapping the lengths)
+ *   totals        int32 [4] output: tokens, longest context, free blocks left, status
+ * The lengths are checked on the device.  A step that the host call would
+ * refuse (a negative computed length, a row wider than max_blocks_per_seq, more
+ * than max_tokens tokens: PHOTON_ERR_INVALID_ARG; too few free blocks:
+ * PHOTON_ERR_POOL_EXHAUSTED) leaves block_tables, free_blocks and the pool as
+ * they were, sets totals[3] to that status and PHOTON_DEVERR_METADATA, and
+ * emits an empty step (no tokens, all contexts 0).  A block id outside the
+ * pool gives its tokens slot -1 and sets PHOTON_DEVERR_BLOCK_RANGE.
+ * block_size 16; num_seqs <= 16384 and num_seqs * max_blocks_per_seq < 2^31
+ * (PHOTON_ERR_UNSUPPORTED otherwise).
+ */
+int photon_build_step_metadata_device(const int32_t *num_computed_tokens, const int32_t *num_new_tokens,
+                                      int32_t num_seqs, int32_t block_size, int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, int32_t *free_blocks, int64_t num_blocks,
+                                      const int32_t *num_free, int32_t *num_free_out, int32_t max_tokens,
+                                      int32_t *token_seq, int32_t *positions, int64_t *slot_mapping,
+                                      int32_t *context_lens, int32_t *totals, photon_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Two-phase continuous-batching scheduler (host side).

@@ -19,9 +19,12 @@ import numpy as np
 __all__ = [
     "PhotonError", "F32", "BF16", "ROPE_NEOX", "ROPE_GPTJ", "ROPE_NONE",
     "DEVERR_SLOT_RANGE", "DEVERR_BLOCK_RANGE", "DEVERR_CONTEXT_RANGE", "DEVERR_WAIT_TIMEOUT",
+    "DEVERR_METADATA",
     "lib", "lib_path", "photon_version", "photon_status_string",
     "photon_kv_cache_write", "photon_rope_q_kv_cache_write", "photon_kv_cache_write_fp8",
     "photon_paged_attention_decode_fp8", "photon_paged_attention_partial_fp8",
+    "photon_kv_cache_fp4_record_bytes", "photon_kv_cache_write_fp4", "photon_kv_cache_read_fp4",
+    "photon_paged_attention_decode_fp4", "photon_build_step_metadata_device",
     "photon_paged_attention_prefill",
     "photon_paged_attention_workspace_size",
     "photon_paged_attention_decode", "photon_paged_attention_partial",
@@ -34,6 +37,7 @@ __all__ = [
 F32, BF16 = 0, 1
 ROPE_NEOX, ROPE_GPTJ, ROPE_NONE = 0, 1, 2
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_RANGE, DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
+DEVERR_METADATA = 16
 _ROPE = {"neox": ROPE_NEOX, "gptj": ROPE_GPTJ, "none": ROPE_NONE}
 STATIC_SCRATCH_BYTES = 32 * 1024 * 1024  # PHOTON_STATIC_SCRATCH_BYTES
 
@@ -88,6 +92,18 @@ def lib() -> ctypes.CDLL:
     L.photon_paged_attention_prefill.restype = E
     L.photon_paged_attention_reduce.argtypes = [P, P, i32, i32, i32, i32, i32, E, P, sz, P]
     L.photon_paged_attention_reduce.restype = E
+    L.photon_kv_cache_fp4_record_bytes.argtypes = [i32]
+    L.photon_kv_cache_fp4_record_bytes.restype = sz
+    L.photon_kv_cache_write_fp4.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i64, E, f32, E, P]
+    L.photon_kv_cache_write_fp4.restype = E
+    L.photon_kv_cache_read_fp4.argtypes = [P, P, P, P, i32, i32, i32, i32, i64, E, P]
+    L.photon_kv_cache_read_fp4.restype = E
+    L.photon_paged_attention_decode_fp4.argtypes = [P, P, P, P, f32, P, i32, i32, i32, i32, i32, i64, i32,
+                                                    i32, i32, E, P, sz, P]
+    L.photon_paged_attention_decode_fp4.restype = E
+    L.photon_build_step_metadata_device.argtypes = [P, P, i32, i32, P, i32, P, i64, P, P, i32, P, P, P, P,
+                                                    P, P]
+    L.photon_build_step_metadata_device.restype = E
     L.photon_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32), E]
     L.photon_device_errors.restype = E
     L.photon_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P]
@@ -288,6 +304,109 @@ def photon_paged_attention_prefill(q, token_seq, positions, k_cache, v_cache, bl
         float(scale), _p(out), T, block_tables.shape[0], Hq, Hkv, d, bs, nb, block_tables.shape[1],
         int(max_position), int(partition_size), _dt(k_cache), _dt(out), _p(workspace), ws_bytes,
         _stream(stream)), "photon_paged_attention_prefill")
+
+
+# ---- 4-bit (E2M1) KV cache ------------------------------------------------------
+
+def photon_kv_cache_fp4_record_bytes(head_dim: int) -> int:
+    """Bytes of one (block, KV head) record of a 4-bit pool (0: no such head_dim)."""
+    return int(lib().photon_kv_cache_fp4_record_bytes(int(head_dim)))
+
+
+def _want(what, t, dtype, shape=None):
+    """Raises unless t is a device tensor of this dtype (and shape)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _fp4_pool(kv_cache, H, d):
+    import torch
+    _want("kv_cache", kv_cache, torch.uint8)
+    if kv_cache.dim() != 3 or kv_cache.shape[1] != H or kv_cache.shape[2] != 17 * d:
+        raise ValueError(f"kv_cache must be [num_blocks, {H}, {17 * d}], got {tuple(kv_cache.shape)}")
+    return kv_cache.shape[0]
+
+
+def photon_kv_cache_write_fp4(k, v, positions, slot_mapping, kv_cache, rope_theta, rope_style="neox",
+                              stream=None):
+    """4-bit write: k, v [T, H_kv, d] (float32 or bfloat16); positions int32
+    [T]; slot_mapping int64 [T]; kv_cache uint8 [num_blocks, H_kv, 17 * d]."""
+    import torch
+    T, H, d = k.shape
+    nb = _fp4_pool(kv_cache, H, d)
+    _want("k", k, k.dtype)
+    _want("v", v, k.dtype, k.shape)
+    _want("positions", positions, torch.int32, (T,))
+    _want("slot_mapping", slot_mapping, torch.int64, (T,))
+    style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
+    _check(lib().photon_kv_cache_write_fp4(_p(k), _p(v), _p(positions), _p(slot_mapping), _p(kv_cache), T, H,
+                                           d, 16, nb, _dt(k), float(rope_theta), style, _stream(stream)),
+           "photon_kv_cache_write_fp4")
+
+
+def photon_kv_cache_read_fp4(kv_cache, slot_mapping, k, v, stream=None):
+    """Dequantised rows of the tokens at slot_mapping (int64 [T]) into k and v
+    [T, H_kv, d] (float32 or bfloat16)."""
+    import torch
+    T, H, d = k.shape
+    nb = _fp4_pool(kv_cache, H, d)
+    _want("k", k, k.dtype)
+    _want("v", v, k.dtype, k.shape)
+    _want("slot_mapping", slot_mapping, torch.int64, (T,))
+    _check(lib().photon_kv_cache_read_fp4(_p(kv_cache), _p(slot_mapping), _p(k), _p(v), T, H, d, 16, nb, _dt(k),
+                                          _stream(stream)), "photon_kv_cache_read_fp4")
+
+
+def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
+                                      partition_size=512, workspace=None, stream=None):
+    """Decode attention over a 4-bit pool (see photon_kv_cache_write_fp4); q
+    bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
+    import torch
+    B, Hq, d = q.shape
+    Hkv = kv_cache.shape[1]
+    nb = _fp4_pool(kv_cache, Hkv, d)
+    _want("q", q, torch.bfloat16)
+    _want("out", out, out.dtype, q.shape)
+    _want("block_tables", block_tables, torch.int32, (B, block_tables.shape[1]))
+    _want("context_lens", context_lens, torch.int32, (B,))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().photon_paged_attention_decode_fp4(
+        _p(q), _p(kv_cache), _p(block_tables), _p(context_lens), float(scale), _p(out), B, Hq, Hkv, d, 16, nb,
+        block_tables.shape[1], int(max_context_len), int(partition_size), _dt(out), _p(workspace), ws_bytes,
+        _stream(stream)), "photon_paged_attention_decode_fp4")
+
+
+def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block_tables, free_blocks, num_free,
+                                      token_seq, positions, slot_mapping, context_lens, totals,
+                                      num_free_out=None, block_size=16, stream=None):
+    """photon_build_step_metadata on the GPU (all arguments device tensors):
+    block_tables int32 [B, max_blocks] and the free-block stack free_blocks
+    int32 [num_blocks] / num_free int32 [1] are updated in place (the new count
+    into num_free_out if given); num_new_tokens[s] < 0 releases row s.  Fills
+    token_seq, positions (int32) and slot_mapping (int64), all [max_tokens],
+    context_lens int32 [B] and totals int32 [4] (tokens, longest context, free
+    blocks, status)."""
+    import torch
+    B, W = block_tables.shape
+    M = token_seq.shape[0]
+    num_free_out = num_free if num_free_out is None else num_free_out
+    i32 = torch.int32
+    for what, t, shape in (("num_computed_tokens", num_computed_tokens, (B,)),
+                           ("num_new_tokens", num_new_tokens, (B,)), ("block_tables", block_tables, (B, W)),
+                           ("free_blocks", free_blocks, free_blocks.shape), ("num_free", num_free, (1,)),
+                           ("num_free_out", num_free_out, (1,)), ("token_seq", token_seq, (M,)),
+                           ("positions", positions, (M,)), ("context_lens", context_lens, (B,)),
+                           ("totals", totals, (4,))):
+        _want(what, t, i32, shape)
+    _want("slot_mapping", slot_mapping, torch.int64, (M,))
+    _check(lib().photon_build_step_metadata_device(
+        _p(num_computed_tokens), _p(num_new_tokens), B, int(block_size), _p(block_tables), W, _p(free_blocks),
+        free_blocks.numel(), _p(num_free), _p(num_free_out), M, _p(token_seq), _p(positions),
+        _p(slot_mapping), _p(context_lens), _p(totals), _stream(stream)), "photon_build_step_metadata_device")
 
 
 def photon_paged_attention_reduce(context_lens, out, max_context_len, partition_size=512,

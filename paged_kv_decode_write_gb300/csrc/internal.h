@@ -46,6 +46,38 @@ struct DecodeCtl {
 constexpr int kCtlCountBits = 24;
 constexpr unsigned long long kCtlTag = 0x9e3779b97full << kCtlCountBits;
 
+// Read of 4-bit cache rows back to a floating type.
+struct Fp4ReadArgs {
+  const void *pool;
+  const int64_t *slot_mapping;
+  void *k_out;
+  void *v_out;
+  int64_t num_slots;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+};
+
+// Step metadata on the device (photon_build_step_metadata_device).
+constexpr int kStepMetaMaxSeqs = 16384;  // three prefix sums of int32 in shared memory
+struct StepMetaArgs {
+  const int32_t *num_computed;
+  const int32_t *num_new;
+  int32_t *block_tables;
+  int32_t *free_blocks;
+  const int32_t *num_free;
+  int32_t *num_free_out;
+  int32_t *token_seq;
+  int32_t *positions;
+  int64_t *slot_mapping;
+  int32_t *context_lens;
+  int32_t *totals;
+  int64_t num_blocks;
+  int32_t num_seqs;
+  int32_t max_blocks_per_seq;
+  int32_t max_tokens;
+};
+
 struct DecodeArgs {
   const void *q;
   const void *k_cache;
@@ -123,6 +155,12 @@ cudaError_t launch_kv_cache_write_fp8(const WriteArgs &a, photon_dtype in_dt, co
                                       const float *v_scale, unsigned int *err, cudaStream_t st);
 cudaError_t launch_decode_partial_fp8(const DecodeArgs &a, const float *k_scale,
                                       const float *v_scale, unsigned int *err, cudaStream_t st);
+cudaError_t launch_kv_cache_write_fp4(const WriteArgs &a, photon_dtype in_dt, unsigned int *err,
+                                      cudaStream_t st);
+cudaError_t launch_kv_cache_read_fp4(const Fp4ReadArgs &a, photon_dtype out_dt, unsigned int *err,
+                                     cudaStream_t st);
+cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st);
+cudaError_t launch_step_metadata(const StepMetaArgs &a, unsigned int *err, cudaStream_t st);
 
 // Every host-side check of photon_paged_attention_decode except the workspace
 // one: PHOTON_OK or the status that call would return, nothing launched.

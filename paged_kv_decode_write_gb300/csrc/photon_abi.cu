@@ -555,3 +555,141 @@ int photon_device_errors(uint32_t *flags_out, int clear) {
 }
 
 }  // extern "C"
+
+// ---- 4-bit (E2M1) KV cache, step metadata on the device --------------------
+
+namespace photon {
+namespace {
+
+// Shape checks shared by the 4-bit calls (record pool of num_blocks blocks).
+int check_fp4_pool(int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks) {
+  if (num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PHOTON_ERR_INVALID_ARG;
+  if (block_size != kBlockSize) return PHOTON_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PHOTON_ERR_UNSUPPORTED;
+  if (num_blocks > INT64_MAX / (static_cast<int64_t>(num_kv_heads) * 17 * head_dim))
+    return PHOTON_ERR_INVALID_ARG;
+  return PHOTON_OK;
+}
+
+}  // namespace
+}  // namespace photon
+
+extern "C" {
+
+size_t photon_kv_cache_fp4_record_bytes(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? static_cast<size_t>(17 * head_dim) : 0;
+}
+
+int photon_kv_cache_write_fp4(const void *k, const void *v, const int32_t *positions,
+                              const int64_t *slot_mapping, void *kv_cache, int32_t num_tokens,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                              int64_t num_blocks, photon_dtype in_dtype, float rope_theta,
+                              photon_rope rope_style, photon_stream_t stream) {
+  if (num_tokens < 0) return PHOTON_ERR_INVALID_ARG;
+  if (in_dtype != PHOTON_F32 && in_dtype != PHOTON_BF16) return PHOTON_ERR_INVALID_ARG;
+  if (rope_style != PHOTON_ROPE_NEOX && rope_style != PHOTON_ROPE_GPTJ &&
+      rope_style != PHOTON_ROPE_NONE)
+    return PHOTON_ERR_INVALID_ARG;
+  if (rope_style != PHOTON_ROPE_NONE && !(std::isfinite(rope_theta) && rope_theta > 0.f))
+    return PHOTON_ERR_INVALID_ARG;
+  const int rc = photon::check_fp4_pool(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PHOTON_OK || num_tokens == 0) return rc;
+  if (!k || !v || !positions || !slot_mapping || !kv_cache) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(positions, 4) ||
+      !aligned(slot_mapping, 8))
+    return PHOTON_ERR_INVALID_ARG;
+  WriteArgs a{};
+  a.k = k;
+  a.v = v;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = kv_cache;
+  a.num_slots = num_blocks * block_size;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.rope_style = rope_style;
+  for (int i = 0; i < head_dim / 2; ++i)
+    a.inv_freq[i] = std::pow(static_cast<double>(rope_theta), -2.0 * i / head_dim);
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  return cuda_status(launch_kv_cache_write_fp4(a, in_dtype, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int photon_kv_cache_read_fp4(const void *kv_cache, const int64_t *slot_mapping, void *k, void *v,
+                             int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int64_t num_blocks, photon_dtype out_dtype,
+                             photon_stream_t stream) {
+  if (num_tokens < 0) return PHOTON_ERR_INVALID_ARG;
+  if (out_dtype != PHOTON_F32 && out_dtype != PHOTON_BF16) return PHOTON_ERR_INVALID_ARG;
+  const int rc = photon::check_fp4_pool(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PHOTON_OK || num_tokens == 0) return rc;
+  if (!kv_cache || !slot_mapping || !k || !v) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slot_mapping, 8))
+    return PHOTON_ERR_INVALID_ARG;
+  Fp4ReadArgs a{kv_cache, slot_mapping, k, v, num_blocks * block_size, num_tokens, num_kv_heads, head_dim};
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  return cuda_status(launch_kv_cache_read_fp4(a, out_dtype, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const int32_t *block_tables,
+                                      const int32_t *context_lens, float scale, void *out,
+                                      int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                      int32_t max_blocks_per_seq, int32_t max_context_len,
+                                      int32_t partition_size, photon_dtype out_dtype, void *workspace,
+                                      size_t workspace_bytes, photon_stream_t stream) {
+  Prepared p{};
+  int rc = prepare_decode(q, kv_cache, kv_cache, block_tables, context_lens, scale, out, num_seqs,
+                          num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                          max_blocks_per_seq, max_context_len, partition_size, PHOTON_BF16,
+                          out_dtype, workspace, workspace_bytes, &p);
+  if (rc != PHOTON_OK) return rc;
+  rc = photon::check_fp4_pool(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PHOTON_OK || num_seqs == 0) return rc;
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = cuda_status(launch_decode_partial_fp4(p.args, err, st));
+  if (rc != PHOTON_OK || p.ws.total == 0) return rc;
+  return cuda_status(launch_decode_reduce(p.args, st));
+}
+
+int photon_build_step_metadata_device(const int32_t *num_computed_tokens, const int32_t *num_new_tokens,
+                                      int32_t num_seqs, int32_t block_size, int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, int32_t *free_blocks, int64_t num_blocks,
+                                      const int32_t *num_free, int32_t *num_free_out, int32_t max_tokens,
+                                      int32_t *token_seq, int32_t *positions, int64_t *slot_mapping,
+                                      int32_t *context_lens, int32_t *totals, photon_stream_t stream) {
+  if (num_seqs < 0 || block_size <= 0 || max_blocks_per_seq <= 0 || max_tokens < 0 || num_blocks <= 0)
+    return PHOTON_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || num_blocks > INT32_MAX || num_seqs > kStepMetaMaxSeqs ||
+      static_cast<int64_t>(num_seqs) * max_blocks_per_seq > INT32_MAX)
+    return PHOTON_ERR_UNSUPPORTED;
+  if (!free_blocks || !num_free || !num_free_out || !totals) return PHOTON_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!num_computed_tokens || !num_new_tokens || !block_tables || !context_lens))
+    return PHOTON_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (!token_seq || !positions || !slot_mapping)) return PHOTON_ERR_INVALID_ARG;
+  for (const void *ptr : {static_cast<const void *>(num_computed_tokens), static_cast<const void *>(num_new_tokens),
+                          static_cast<const void *>(block_tables), static_cast<const void *>(free_blocks),
+                          static_cast<const void *>(num_free), static_cast<const void *>(num_free_out),
+                          static_cast<const void *>(token_seq), static_cast<const void *>(positions),
+                          static_cast<const void *>(context_lens), static_cast<const void *>(totals)})
+    if (!aligned(ptr, 4)) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned(slot_mapping, 8)) return PHOTON_ERR_INVALID_ARG;
+  // the lengths are read while context_lens is written
+  auto overlap = [n = static_cast<int64_t>(num_seqs)](const int32_t *x, const int32_t *y) {
+    return n > 0 && x < y + n && y < x + n;
+  };
+  if (overlap(context_lens, num_computed_tokens) || overlap(context_lens, num_new_tokens))
+    return PHOTON_ERR_INVALID_ARG;
+  StepMetaArgs a{num_computed_tokens, num_new_tokens, block_tables, free_blocks, num_free, num_free_out,
+                 token_seq, positions, slot_mapping, context_lens, totals, num_blocks, num_seqs,
+                 max_blocks_per_seq, max_tokens};
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  return cuda_status(launch_step_metadata(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,372 @@
+"""4-bit (E2M1) KV cache on the GPU: write, read and decode against the
+oracle's definitions (oracle/fp4.py), and the step a program makes of them."""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+from oracle import fp4
+from tests.helpers import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _dev(a):
+    return _torch().from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _storage(x, dtype):
+    """A float array as storage: float32, or bf16 bits (uint16) and its tensor."""
+    torch = _torch()
+    t = torch.from_numpy(np.ascontiguousarray(x, np.float32))
+    t = t if dtype == "f32" else t.bfloat16()
+    return synth.to_storage_numpy(t), t.cuda()
+
+
+def _random_pool(rng, nb, H, d, std=0.5):
+    """Pool of random codes and bf16 scales of about std / 3."""
+    byte, nib, sb = fp4.record_positions(d)
+    pool = rng.integers(0, 256, (nb, H, 17 * d), dtype=np.uint8)
+    sc = np.abs(rng.standard_normal((2, 16, d // 64) + (nb, H)) * std / 3 + std / 6).astype(np.float32)
+    bits = (sc.view(np.uint32) >> 16).astype(np.uint16)
+    for w in range(2):
+        pool[:, :, sb[w]] = np.moveaxis(bits[w] & 0xFF, (0, 1), (2, 3)).astype(np.uint8)
+        pool[:, :, sb[w] + 1] = np.moveaxis(bits[w] >> 8, (0, 1), (2, 3)).astype(np.uint8)
+    return pool
+
+
+def _tables(rng, ctx, nb, width=None):
+    need = [-(-max(int(c), 0) // 16) for c in ctx]
+    perm = rng.permutation(nb)
+    W = max(1, max(need)) if width is None else width
+    bt = np.full((len(ctx), W), -1, np.int32)
+    at = 0
+    for i, n in enumerate(need):
+        bt[i, :n] = perm[at:at + n]
+        at += n
+    return bt
+
+
+def _decode(pk, q, pool, bt, ctx, scale, out_dtype, part, max_ctx=None, extra_rows=0):
+    torch = _torch()
+    B, Hq, d = q.shape
+    mc = int(max(max(ctx), 1)) if max_ctx is None else max_ctx
+    n = pk.photon_paged_attention_workspace_size(B, Hq, d, mc, part)
+    ws = torch.randint(0, 256, (max(n, 1),), dtype=torch.uint8, device="cuda") if n else None
+    out = torch.full((B + extra_rows, Hq, d), -7.0, dtype=out_dtype, device="cuda")
+    pk.photon_paged_attention_decode_fp4(q, pool, _dev(bt), _dev(np.asarray(ctx, np.int32)), scale, out[:B], mc, part, ws)
+    torch.cuda.synchronize()
+    return out
+
+
+def _tolerance(q64, kd, vd, ctx, scale, out_bf16, ref):
+    """Per output element.  Let V = max |v|.  A relative error e of a weight
+    moves a weighted mean by at most 2 e V (numerator and denominator), one of
+    the numerator's weights alone by e V.
+      score: products of f16 by exact codes summed in fp32, at most d + 4
+        roundings of 2^-24 (2^-23 where the tensor core truncates) of
+        sum |q||k|, times the scale; ex2 within 2^-22
+      weight times V scale in f16: 2^-12 (bf16 output) or f16 + remainder 2^-22
+      sums over n tokens in fp32, one rounding per 16-token MMA: (n / 16 + 8) 2^-23
+      output: half a step of the type, 2^-8 or 2^-24 of the value"""
+    d = q64.shape[-1]
+    V = np.abs(vd).max() if vd.size else 0.0
+    qk = np.abs(q64).sum(-1).max() * np.abs(kd).max()
+    e_score = abs(scale) * (d + 4) * 2.0 ** -23 * qk + 2.0 ** -22
+    e_sum = (max(ctx) / 16 + 8) * 2.0 ** -23
+    e_p = 2.0 ** -12 if out_bf16 else 2.0 ** -22
+    return V * (2 * e_score + 2 * e_sum + e_p) + np.abs(ref) * (2.0 ** -8 if out_bf16 else 2.0 ** -24)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("style", ["neox", "gptj", "none"])
+@pytest.mark.parametrize("T,H", [(1, 1), (5, 3), (37, 8), (70, 4)])
+def test_write_codes_equal_the_oracle(T, H, style, dtype, d):
+    """Every byte of the pool: codes and scales of the written tokens bit for
+    bit, all other bytes as they were; slots -1 and past the pool write nothing."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(T * 10 + H + d)
+    nb = 12
+    k, kt = _storage(rng.standard_normal((T, H, d)) * 0.7, dtype)
+    v, vt = _storage(rng.standard_normal((T, H, d)) * rng.lognormal(0, 3, (T, H, 1)), dtype)
+    slots = rng.permutation(nb * 16)[:T].astype(np.int64)
+    slots[T // 2::7] = -1
+    pos = rng.integers(0, 100000, T).astype(np.int32)
+    want = rng.integers(0, 256, (nb, H, 17 * d), dtype=np.uint8)
+    pool = _dev(want.copy())
+    gpu_slots = slots.copy()
+    if T > 4:
+        gpu_slots[slots < 0] = np.where(np.arange((slots < 0).sum()) % 2, nb * 16 + 3, -1)
+    pk.photon_device_errors()
+    pk.photon_kv_cache_write_fp4(kt, vt, _dev(pos), _dev(gpu_slots), pool, 5e5, style)
+    fp4.write(k, v, pos, slots, want, 5e5, {"neox": 0, "gptj": 1, "none": 2}[style])
+    assert np.array_equal(pool.cpu().numpy(), want)
+    assert pk.photon_device_errors() == (pk.DEVERR_SLOT_RANGE if (gpu_slots >= nb * 16).any() else 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_midpoints_and_special_groups(d):
+    """fp32 rows whose quotient by the group's scale is exactly a midpoint, or
+    one unit beside it; groups of zeros, of subnormals, of huge values, with an
+    infinity or a NaN."""
+    pk = ensure_built()
+    rng = np.random.default_rng(d)
+    T, H, nb = 32, 2, 2
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    x = np.zeros((T, H, d), np.float32)
+    for t in range(T):
+        for h in range(H):
+            for g in range(d // 64):
+                s = float(np.float32(rng.integers(128, 256)) * np.float32(2.0) ** int(rng.integers(-90, 100)))
+                y = (mids[rng.integers(0, 7, 64)] * rng.choice([-1, 1], 64) * s).astype(np.float32)
+                nudge = rng.integers(0, 3, 64)
+                y = np.where(nudge == 1, np.nextafter(y, np.float32(np.inf)),
+                             np.where(nudge == 2, np.nextafter(y, np.float32(-np.inf)), y))
+                y[rng.integers(0, 64)] = np.float32(6 * s)
+                x[t, h, 64 * g:64 * g + 64] = y
+    x[0] = 0
+    x[1] = rng.standard_normal((H, d)).astype(np.float32) * np.float32(2.0 ** -132)
+    x[2, 0, 5], x[3, 1, 7], x[4, 0, 9] = np.inf, np.nan, -np.inf
+    x[5] = np.float32(3.0e38) * rng.choice([-1, 1, 0.5], (H, d))
+    slots = rng.permutation(nb * 16).astype(np.int64)
+    pos = np.zeros(T, np.int32)
+    want = np.zeros((nb, H, 17 * d), np.uint8)
+    pool = _dev(want.copy())
+    pk.photon_kv_cache_write_fp4(_dev(x), _dev(-x), _dev(pos), _dev(slots), pool, 1e4, "none")
+    fp4.write(x, -x, pos, slots, want, 1e4, oracle.ROPE_NONE)
+    kd, vd = fp4.dequant(want, d)
+    kg, vg = fp4.dequant(pool.cpu().numpy(), d)
+    assert np.array_equal(kg, kd, equal_nan=True) and np.array_equal(vg, vd, equal_nan=True)
+    blk, off = slots // 16, slots % 16
+    assert np.isnan(kg[blk[2], 0, off[2], :64]).all() and np.isnan(vg[blk[3], 1, off[3], :64]).all()
+    assert np.isfinite(kg[blk[5], :, off[5]]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(1, 1), (33, 3), (200, 8)])
+def test_read_returns_the_rounded_values(T, H, dtype, d):
+    """Bit for bit the product rounded once; repeated slots; rows of slots -1
+    or past the pool left as they were."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(T + d)
+    nb = 6
+    pool = _random_pool(rng, nb, H, d)
+    slots = rng.integers(0, nb * 16, T).astype(np.int64)
+    skip = np.zeros(T, bool)
+    if T > 1:
+        skip[1::9] = True
+        slots[1::18], slots[10::18] = -1, nb * 16
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    k = torch.full((T, H, d), -3.0, dtype=dt, device="cuda")
+    v = torch.full((T, H, d), -3.0, dtype=dt, device="cuda")
+    pk.photon_device_errors()
+    pk.photon_kv_cache_read_fp4(_dev(pool), _dev(slots), k, v)
+    torch.cuda.synchronize()
+    for got, val in zip((k, v), fp4.dequant(pool, d)):
+        want = val[np.clip(slots, 0, nb * 16 - 1) // 16, :, np.clip(slots, 0, nb * 16 - 1) % 16]
+        want = torch.from_numpy(np.where(skip[:, None, None], -3.0, want)).float().to(dt)
+        assert torch.equal(got.cpu(), want)
+    assert pk.photon_device_errors() == (pk.DEVERR_SLOT_RANGE if (slots >= nb * 16).any() else 0)
+
+
+CONTEXTS = [([1, 17, 600, 1500, 33, 0], 256), ([3000, 9, 700, 0, 16], 512),
+            ([16, 31, 32, 33, 47, 48, 49, 63, 64, 65, 511, 512, 513, 15], 64), ([1024], 32), ([5], 512), ([130, 0], 16)]
+
+
+@pytest.mark.parametrize("ctx,part", CONTEXTS)
+@pytest.mark.parametrize("H,G", [(8, 1), (8, 2), (8, 4), (4, 8), (1, 4), (3, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_decode_matches_the_oracle(ctx, part, H, G, d, out):
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(sum(ctx) + H * G + d)
+    nb = sum(-(-c // 16) for c in ctx) + 3
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
+    scale = d ** -0.5
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, dt, part, extra_rows=2)
+    ref = fp4.paged_attention(q, pool, bt, ctx, scale)
+    assert (got[len(ctx):] == -7.0).all()                  # rows behind the batch
+    got = got[:len(ctx)].double().cpu().numpy()
+    kd, vd = fp4.dequant(pool, d)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, scale, out == "bf16", ref)).all()
+    for s, c in enumerate(ctx):
+        if c == 0:
+            assert (got[s] == 0).all()
+    assert pk.photon_device_errors() == 0
+
+
+@pytest.mark.parametrize("qexp,vexp,scale", [(0, 0, -0.3), (100, 0, 2.0 ** -103), (-100, 0, 2.0 ** 97), (126, 0, 0.0), (123, 0, 2.0 ** -126), (120, 0, 0.0),
+                                             (0, 60, 0.125), (0, -100, 0.125), (3, -60, -0.01), (-130, 0, 0.5)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_is_scale_free(qexp, vexp, scale, d):
+    """q and V scales of any magnitude, a negative or zero softmax scale."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(7)
+    ctx, H, G = [300, 40, 1], 2, 4
+    nb = 30
+    pool = _random_pool(rng, nb, H, d)
+    byte, nib, sb = fp4.record_positions(d)
+    lo, hi = pool[:, :, sb[1]].astype(np.uint16), pool[:, :, sb[1] + 1].astype(np.uint16)
+    bits = (lo | (hi << 8)).astype(np.int64) + (vexp << 7)
+    bits = np.where(rng.random(bits.shape) < 0.2, 0, bits).astype(np.uint16)     # groups of zeros
+    pool[:, :, sb[1]], pool[:, :, sb[1] + 1] = bits & 0xFF, bits >> 8
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((3, H * G, d)) * 2.0 ** qexp, "bf16")
+    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, torch.float32, 64).double().cpu().numpy()
+    ref = fp4.paged_attention(q, pool, bt, ctx, float(np.float32(scale)))
+    kd, vd = fp4.dequant(pool, d)
+    # 2^126 times a normal value of 4 or more is an infinity in bf16: rows whose q holds one are NaN in the
+    # definition too (infinity times the zero scale)
+    fine = np.isfinite(ref)
+    assert np.array_equal(np.isfinite(got), fine) and (fine.all() or qexp == 126)
+    q64 = np.where(np.isfinite(oracle.to_f64(q)), oracle.to_f64(q), 0.0)
+    off = np.abs(got - ref)[fine]
+    assert (off <= (_tolerance(q64, kd, vd, ctx, scale, False, ref) + 2.0 ** -149)[fine]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("part", [32, 512])
+def test_decode_ignores_everything_past_the_context(d, part):
+    """NaN and infinite scales behind the last token, in the page's tail and in
+    unused blocks, leave every bit of the output as it was."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(d + part)
+    ctx, H, G = [1, 15, 37, 200, 449, 64], 2, 4
+    nb = 80
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb, width=32)
+    _, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
+    a = _decode(pk, qt, _dev(pool), bt, ctx, 0.2, torch.float32, part)
+    byte, nib, sb = fp4.record_positions(d)
+    bad = np.ones((nb, 16), bool)
+    for s, c in enumerate(ctx):
+        for p in range(c):
+            bad[bt[s, p // 16], p % 16] = False
+    for b, r in zip(*np.nonzero(bad)):
+        for w in range(2):
+            pool[b][:, sb[w, r]] = 0xC0 if (b + r) % 2 else 0x80
+            pool[b][:, sb[w, r] + 1] = 0x7F                     # NaN, +inf
+            pool[b][:, byte[w, r]] = 0xFF
+    b_ = _decode(pk, qt, _dev(pool), bt, ctx, 0.2, torch.float32, part)
+    assert torch.equal(a, b_) and torch.isfinite(a).all()
+    assert pk.photon_device_errors() == 0
+
+
+def test_decode_nan_values_stay_in_their_heads_and_rows():
+    """A token with a NaN V scale makes the outputs of its (sequence, KV head)
+    NaN in the dims of that scale, one with a NaN K scale in all; no others."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(5)
+    d, ctx, H, G, nb = 128, [100, 300, 50], 2, 2, 40
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb)
+    byte, nib, sb = fp4.record_positions(d)
+    pool[bt[0, 2], 1, sb[1, 3, 1]:sb[1, 3, 1] + 2] = [0xFF, 0x7F]
+    pool[bt[1, 4], 0, sb[0, 8, 0]:sb[0, 8, 0] + 2] = [0xFF, 0x7F]
+    _, qt = _storage(rng.standard_normal((3, H * G, d)), "bf16")
+    for part in (64, 512):
+        got = torch.isnan(_decode(pk, qt, _dev(pool), bt, ctx, 0.1, torch.float32, part)).cpu().numpy()
+        want = np.zeros_like(got)
+        want[0, 2:4, 64:] = True
+        want[1, 0:2] = True
+        assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_bad_blocks_and_contexts(d):
+    """Block ids outside the pool are skipped and flagged, a context above the
+    declared bound is clamped and flagged; the rest is as without them."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(d)
+    ctx, H, G, nb = [100, 200, 33, 64], 2, 4, 40
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((4, H * G, d)), "bf16")
+    bad = bt.copy()
+    bad[0, 1], bad[1, 3], bad[1, 12] = nb, -5, 2 ** 30
+    bad[2, :3] = -1                                     # nothing left of sequence 2
+    pk.photon_device_errors()
+    for part in (32, 512):
+        got = _decode(pk, qt, _dev(pool), bad, ctx, 0.2, torch.float32, part).double().cpu().numpy()
+        assert pk.photon_device_errors() == pk.DEVERR_BLOCK_RANGE
+        kd, vd = fp4.dequant(pool, d)
+        q64 = oracle.to_f64(q)
+        for s, c in enumerate(ctx):
+            keep = np.array([0 <= bad[s, p // 16] < nb for p in range(c)])
+            for h in range(H * G):
+                if not keep.any():
+                    assert (got[s, h] == 0).all()
+                    continue
+                ks = np.array([kd[bad[s, p // 16], h // G, p % 16] for p in range(c) if keep[p]])
+                vs = np.array([vd[bad[s, p // 16], h // G, p % 16] for p in range(c) if keep[p]])
+                x = ks @ q64[s, h] * 0.2
+                w = np.exp(x - x.max())
+                ref = w @ vs / w.sum()
+                assert (np.abs(got[s, h] - ref) <= _tolerance(q64, kd, vd, ctx, 0.2, False, ref)).all()
+    long = [100, 10 ** 6, 33, 64]
+    got = _decode(pk, qt, _dev(pool), bt, long, 0.2, torch.float32, 64, max_ctx=208)
+    assert pk.photon_device_errors() & pk.DEVERR_CONTEXT_RANGE
+    same = _decode(pk, qt, _dev(pool), bt, [100, 208, 33, 64], 0.2, torch.float32, 64, max_ctx=208)
+    assert torch.equal(got, same)
+    pk.photon_device_errors()
+
+
+def test_decode_repeats_bit_for_bit():
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(1)
+    ctx = [int(x) for x in rng.integers(1, 4000, 40)]
+    nb = sum(-(-c // 16) for c in ctx)
+    pool = _dev(_random_pool(rng, nb, 4, 64))
+    bt = _tables(rng, ctx, nb)
+    _, qt = _storage(rng.standard_normal((40, 16, 64)), "bf16")
+    a = _decode(pk, qt, pool, bt, ctx, 0.125, torch.float32, 128)
+    for _ in range(5):
+        assert torch.equal(a, _decode(pk, qt, pool, bt, ctx, 0.125, torch.float32, 128))
+
+
+def test_large_pool_offsets():
+    """Records past 2^32 bytes: written, read back and attended to."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(2)
+    d, H = 128, 8
+    nb = 2 ** 32 // (17 * d * H) + 40
+    pool = torch.zeros(nb, H, 17 * d, dtype=torch.uint8, device="cuda")
+    ctx = [50]
+    bt = np.array([[nb - 1, 3, nb - 7, nb - 2]], np.int32)
+    pos = np.arange(50, dtype=np.int32)
+    slots = bt[0, pos // 16].astype(np.int64) * 16 + pos % 16
+    k, kt = _storage(rng.standard_normal((50, H, d)), "bf16")
+    v, vt = _storage(rng.standard_normal((50, H, d)), "bf16")
+    pk.photon_kv_cache_write_fp4(kt, vt, _dev(pos), _dev(slots), pool, 1e4)
+    small = np.zeros((4, H, 17 * d), np.uint8)
+    fp4.write(k, v, pos, np.arange(50, dtype=np.int64), small, 1e4)
+    assert np.array_equal(pool[bt[0].tolist()].cpu().numpy(), small)
+    ko, vo = torch.empty_like(kt, dtype=torch.float32), torch.empty_like(vt, dtype=torch.float32)
+    pk.photon_kv_cache_read_fp4(pool, _dev(slots), ko, vo)
+    kd, vd = fp4.dequant(small, d)
+    assert np.array_equal(ko.cpu().numpy(), kd[pos // 16, :, pos % 16].astype(np.float32))
+    q, qt = _storage(rng.standard_normal((1, 16, d)), "bf16")
+    got = _decode(pk, qt, pool, bt, ctx, 0.1, torch.float32, 512).double().cpu().numpy()
+    ref = fp4.paged_attention(q, small, np.arange(4, dtype=np.int32)[None], ctx, 0.1)
+    assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, 0.1, False, ref)).all()
+    assert pk.photon_device_errors() == 0
