@@ -36,6 +36,9 @@ constexpr int kFp4Warps = 4;
 // Least exponent of the V scales that P follows: p is then at most 2^103 and
 // its sum over a context stays in fp32.
 constexpr int kFp4MinExp = -90;
+// Base-2 distance that a score may pass the reference maximum by before the
+// reference moves: a weight times its V scale stays below 2^14 either way.
+constexpr float kFp4Slack = 6.f;
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -49,6 +52,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same into fresh accumulators.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -112,7 +131,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
   // page 32 k + j, `there` which of them exist with a block id in the pool;
   // the next window's ids are on their way.
   uint32_t row = 0, there = 0, valid_bits = 0;
-  int ahead = -1, p_slot = 0, c_slot = 0;
+  int ahead = -1, c_slot = 0;
   uint32_t c_phase = 0;
   auto table_entry = [&](int page) -> int {
     return page < prod.n_pages
@@ -121,9 +140,10 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
   };
   if (prod.valid) ahead = table_entry(lane);
 
-  // Starts the copies of the producer's next step: the lanes of its pages in
-  // the window each copy their record.  False past the warp's last step.
-  auto issue_next = [&]() -> bool {
+  // Starts the copies of the producer's next step into ring slot `slot`: the
+  // lanes of its pages in the window each copy their record.  False past the
+  // warp's last step.
+  auto issue_next = [&](int slot) -> bool {
     while (prod.valid && prod.page >= prod.n_pages) {
       walker_next<BAL>(prod, a, lane, err, total_warps);
       if (prod.valid) ahead = table_entry(lane);
@@ -139,22 +159,21 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
       ahead = table_entry(prod.page + 32 + lane);
     }
     const uint32_t v = (there >> at) & ((1u << PP) - 1);
-    valid_bits = (valid_bits & ~(((1u << PP) - 1) << (PP * p_slot))) | (v << (PP * p_slot));
-    if (lane == 0) mbar_arrive_expect_tx(&bars[p_slot], __popc(v) * REC);
+    valid_bits = (valid_bits & ~(((1u << PP) - 1) << (PP * slot))) | (v << (PP * slot));
+    if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(v) * REC);
     const int i = lane - at;
     if (i >= 0 && i < PP && (v >> i & 1u)) {
       fence_proxy_async_smem();
-      bulk_copy_g2s(stages + p_slot * R::STAGE + i * REC,
+      bulk_copy_g2s(stages + slot * R::STAGE + i * REC,
                     static_cast<const unsigned char *>(a.k_cache) + static_cast<int64_t>(row) * REC, REC,
-                    &bars[p_slot], policy);
+                    &bars[slot], policy);
     }
     prod.page += PP;
-    if (++p_slot == ST) p_slot = 0;
     return true;
   };
 #pragma unroll 1
   for (int k = 0; k < ST; ++k)
-    if (!issue_next()) break;
+    if (!issue_next(k)) break;
 
   while (w.valid) {
     // ---- a new item: the query group
@@ -207,8 +226,11 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
     for (int hh = 0; hh < HH; ++hh)
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) o[hh][mt][0] = o[hh][mt][1] = o[hh][mt][2] = o[hh][mt][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // weights are kept relative to m_ref; m_lim, e_lim: the largest scores and
+    // bits of a V scale that need no new reference
+    float m_lim[2] = {-INFINITY, -INFINITY}, m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     int e_run = kFp4MinExp;
+    uint32_t e_lim = 0;
 
     while (w.page < w.n_pages) {
       const bool landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[c_slot], c_phase, kWaitBudgetCycles));
@@ -233,9 +255,10 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
           e2m1x8_to_f16(kr.y, k0[1]);
           e2m1x8_to_f16(kr.z, k1[0]);
           e2m1x8_to_f16(kr.w, k1[1]);
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          float acc[4];
+          mma_f16_first(acc, k0[0][0], k1[0][0], k0[0][1], k1[0][1], qb[hh][0][0], qb[hh][0][1]);
 #pragma unroll
-          for (int kt = 0; kt < 4; ++kt)
+          for (int kt = 1; kt < 4; ++kt)
             mma_f16(acc, k0[kt >> 1][2 * (kt & 1)], k1[kt >> 1][2 * (kt & 1)], k0[kt >> 1][2 * (kt & 1) + 1],
                     k1[kt >> 1][2 * (kt & 1) + 1], qb[hh][kt][0], qb[hh][kt][1]);
           const float s0 = __uint_as_float(__byte_perm(sr.x, 0u, half_sel));
@@ -278,38 +301,53 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
 #pragma unroll
         for (int i = 0; i < PP; ++i) {
           if (i > 0) {
-            m0 = fmaxf(m0, fmaxf(x[i][0], x[i][2]));
-            m1 = fmaxf(m1, fmaxf(x[i][1], x[i][3]));
+            m0 = max3(m0, x[i][0], x[i][2]);
+            m1 = max3(m1, x[i][1], x[i][3]);
           }
 #pragma unroll
           for (int hh = 0; hh < HH; ++hh) sm = max_bf16x2(sm, max_bf16x2(sv[i][hh][0], sv[i][hh][1]));
         }
+        sm = max(sm & 0xffffu, sm >> 16);
+        // The reference moves only when a score passes it by more than
+        // kFp4Slack or a V scale's exponent passes e_run (scales are not negative).
+        if (__any_sync(0xffffffffu, m0 * sl[0] > m_lim[0] || m1 * sl[1] > m_lim[1] || sm >= e_lim)) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-        }
-        // exponent of the step's largest V scale (scales are not negative)
-        const int es = static_cast<int>(__reduce_max_sync(0xffffffffu, max(sm & 0xffffu, sm >> 16)) >> 7) - 127;
-        e_run = max(e_run, min(es, 127));
-        float alpha[2];
+          for (int d = 4; d < 32; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          const int es = static_cast<int>(__reduce_max_sync(0xffffffffu, sm) >> 7) - 127;
+          e_run = max(e_run, min(es, 127));
+          e_lim = static_cast<uint32_t>(e_run + 128) << 7;
+          float alpha[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          m_run[j] = fmaxf(m_run[j], (j ? m1 : m0) * sl[j]);
-          const float ref = m_run[j] + static_cast<float>(e_run - 13);
-          alpha[j] = exp2_approx(m_ref[j] - ref);
-          m_ref[j] = ref;
+          for (int j = 0; j < 2; ++j) {
+            const float m_run = fmaxf(m_lim[j] - kFp4Slack, (j ? m1 : m0) * sl[j]);
+            m_lim[j] = m_run + kFp4Slack;
+            const float ref = m_run + (static_cast<float>(e_run) - (13.f - kFp4Slack));
+            alpha[j] = exp2_approx(m_ref[j] - ref);
+            m_ref[j] = ref;
+            l_run[j] *= alpha[j];
+          }
+#pragma unroll
+          for (int hh = 0; hh < HH; ++hh)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              o[hh][mt][0] *= alpha[0];
+              o[hh][mt][1] *= alpha[1];
+              o[hh][mt][2] *= alpha[0];
+              o[hh][mt][3] *= alpha[1];
+            }
         }
         uint32_t ph[PP][HH][2], pl[SPLIT ? PP : 1][HH][2];
-        float ps[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < PP; ++i)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const float p0 = exp2_approx(fmaf(x[i][2 * n], sl[0], -m_ref[0]));
             const float p1 = exp2_approx(fmaf(x[i][2 * n + 1], sl[1], -m_ref[1]));
-            ps[0] += p0;
-            ps[1] += p1;
+            l_run[0] += p0;
+            l_run[1] += p1;
 #pragma unroll
             for (int hh = 0; hh < HH; ++hh) {
               const float s = __uint_as_float(__byte_perm(sv[i][hh][n], 0u, half_sel));
@@ -322,19 +360,6 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
               }
             }
           }
-        l_run[0] = fmaf(l_run[0], alpha[0], ps[0]);
-        l_run[1] = fmaf(l_run[1], alpha[1], ps[1]);
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-          for (int hh = 0; hh < HH; ++hh)
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-              o[hh][mt][0] *= alpha[0];
-              o[hh][mt][1] *= alpha[1];
-              o[hh][mt][2] *= alpha[0];
-              o[hh][mt][3] *= alpha[1];
-            }
-        }
         // ---- O^T += V^T P^T: words of tokens 4c .. 4c+3, nibble i = dim 8g + i.
         // Pairing the same nibble of two tokens in one byte gives the f16 pairs
         // (token, token + 1) of the MMA's A operand directly.
@@ -357,11 +382,11 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
           }
       }
       __syncwarp();  // the stage is read before the next copies overwrite it
+      issue_next(c_slot);
       if (++c_slot == ST) {
         c_slot = 0;
         c_phase ^= 1u;
       }
-      issue_next();
     }
 
     // ---- item done: o[hh][mt][2r + j] is head 2c + j, dim 64 hh + 8g + 2mt + r
@@ -448,7 +473,7 @@ cudaError_t launch_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t stre
 cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
   switch (a.head_dim) {
     case 64: return launch_fp4<64, 4, 3, 4>(a, err, st);
-    case 128: return launch_fp4<128, 2, 4, 3>(a, err, st);
+    case 128: return launch_fp4<128, 2, 3, 3>(a, err, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -329,6 +329,37 @@ def test_decode_bad_blocks_and_contexts(d):
     pk.photon_device_errors()
 
 
+@pytest.mark.parametrize("H,G,d", [(8, 4, 64), (1, 8, 64), (3, 2, 128), (8, 2, 128)])
+@pytest.mark.parametrize("kind", ["long", "ragged", "mostly empty"])
+def test_decode_of_full_grids(H, G, d, kind):
+    """Batches that give every warp of the grid several pages and partitions,
+    with empty and one-token sequences, hundreds in a row among them; every
+    call gives the same bits."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(H * 7 + d)
+    total = 16 * 5 * (2432 // H)
+    if kind == "long":
+        ctx = [int(x) for x in rng.integers(total // 8, total // 3, 8)]
+    elif kind == "ragged":
+        ctx = [int(x) for x in np.clip(rng.lognormal(5.5, 1.2, 2 * total // 500), 1, 6000)]
+    else:
+        ctx = [0] * 300 + [int(x) for x in rng.integers(1, 40, 50)] + [0] * 500 + [total] + [0, 1, 0, 16] + [0] * 200
+    nb = sum(-(-c // 16) for c in ctx) + 1
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
+    dev = _dev(pool)
+    a = _decode(pk, qt, dev, bt, ctx, d ** -0.5, torch.float32, 16)
+    for _ in range(4):
+        assert torch.equal(a, _decode(pk, qt, dev, bt, ctx, d ** -0.5, torch.float32, 16))
+    ref = fp4.paged_attention(q, pool, bt, ctx, d ** -0.5)
+    kd, vd = fp4.dequant(pool, d)
+    tol = _tolerance(oracle.to_f64(q), kd, vd, ctx, d ** -0.5, False, ref)
+    assert (np.abs(a.double().cpu().numpy() - ref) <= tol).all()
+    assert pk.photon_device_errors() == 0
+
+
 def test_decode_repeats_bit_for_bit():
     torch = _torch()
     pk = ensure_built()
