@@ -391,9 +391,9 @@ size_t photon_kv_cache_fp4_record_bytes(int32_t head_dim);
 
 /*
  * photon_kv_cache_write_fp4 -- the batched RoPE-fused write into a 4-bit pool.
- * For every token with slot >= 0 and every KV head, y = RoPE(k) (v as it is)
- * rounded once to in_dtype, the value photon_kv_cache_write would store; per
- * 64 dims
+ * For every token with slot >= 0 and every KV head, y = RoPE(k) (v as it is),
+ * the rotation rounded to fp32 and then to in_dtype (before those within about
+ * 2^-36 of the exact one, relative to the pair); per 64 dims
  *   scale = bf16(max |y| / 6)   (the fp32 quotient, both to nearest-even)
  *   code  = nearest E2M1 of y / scale, halves to the even code, |code| <= 6
  * A group of zeros has scale 0; one that holds an infinity or a NaN has a NaN

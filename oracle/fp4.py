@@ -47,6 +47,18 @@ def quantise(y: np.ndarray):
     return codes.reshape(f.shape).astype(np.uint8), bits
 
 
+def rope_rows(k, positions, rope_theta, rope_style=oracle.ROPE_NEOX):
+    """The rotation in fp64, rounded to float32 and then to the storage type."""
+    if rope_style == oracle.ROPE_NONE:
+        return k
+    f = oracle.to_f64(k)
+    y = np.array([[oracle.rope(f[t, h], int(positions[t]), rope_theta, rope_style) for h in range(k.shape[1])]
+                  for t in range(k.shape[0])]).astype(np.float32).reshape(k.shape)
+    if k.dtype == np.float32:
+        return y
+    return np.array([oracle.round_bf16(x) for x in y.ravel().tolist()], np.uint16).reshape(k.shape)
+
+
 def record_positions(d: int):
     """(code byte [2][16][d], nibble [d], scale byte [2][16][d / 64]) of K (0) and V (1)."""
     byte = np.zeros((2, 16, d), np.int64)
@@ -66,7 +78,7 @@ def record_positions(d: int):
 
 def write(k, v, positions, slots, pool, rope_theta, rope_style=oracle.ROPE_NEOX):
     """In-place 4-bit write of storage rows k, v [T, H, d] into pool uint8 [nb, H, 17 d]."""
-    k = oracle.rope_rows(k, positions, rope_theta, rope_style)
+    k = rope_rows(k, positions, rope_theta, rope_style)
     T, H, d = k.shape
     byte, nib, sb = record_positions(d)
     for w, x in enumerate((k, v)):

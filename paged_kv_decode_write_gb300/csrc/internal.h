@@ -46,6 +46,23 @@ struct DecodeCtl {
 constexpr int kCtlCountBits = 24;
 constexpr unsigned long long kCtlTag = 0x9e3779b97full << kCtlCountBits;
 
+// The 4-bit write: angles as fractions of a turn (times 2^64), filled by its launcher.
+constexpr int kFp4MaxTile = 8;  // tokens of a CTA
+struct Fp4WriteArgs {
+  const void *k;
+  const void *v;
+  const int32_t *positions;
+  const int64_t *slot_mapping;
+  void *kv_cache;
+  int64_t num_slots;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t rope_style;
+  int32_t tile;
+  unsigned long long turns[64];
+};
+
 // Read of 4-bit cache rows back to a floating type.
 struct Fp4ReadArgs {
   const void *pool;
