@@ -159,10 +159,20 @@ def _p(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = None  # device index -> handle of its current stream
+
+
 def _stream(stream):
+    """Handle of the given stream, or of the current one (torch's raw getter:
+    building a Stream object for it costs 3 us of a call's 10)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def photon_kv_cache_write(k, v, positions, slot_mapping, k_cache, v_cache, rope_theta,
@@ -313,22 +323,39 @@ def photon_kv_cache_fp4_record_bytes(head_dim: int) -> int:
     return int(lib().photon_kv_cache_fp4_record_bytes(int(head_dim)))
 
 
-def _want(what, t, dtype, shape=None):
-    """Raises unless t is a device tensor of this dtype (and shape)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype != dtype:
+def _arg(what, t, dtype, shape, dev):
+    """Address of t, which must be a contiguous tensor of this dtype (and
+    shape) on the current device."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current CUDA device ({dev}), got {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
+    return t.data_ptr()
 
 
-def _fp4_pool(kv_cache, H, d):
+def _device():
+    """The current CUDA device's index (no tensor is on it, -2, without one)."""
     import torch
-    _want("kv_cache", kv_cache, torch.uint8)
-    if kv_cache.dim() != 3 or kv_cache.shape[1] != H or kv_cache.shape[2] != 17 * d:
-        raise ValueError(f"kv_cache must be [num_blocks, {H}, {17 * d}], got {tuple(kv_cache.shape)}")
-    return kv_cache.shape[0]
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+
+
+def _rows(what, t):
+    """Shape and dtype code of rows [N, heads, head_dim]."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have 3 dimensions, got {tuple(t.shape)}")
+    return t.shape, _dt(t)
+
+
+def _pool(kv_cache, H, d, dev):
+    import torch
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[1] != H or shape[2] != 17 * d:
+        raise ValueError(f"kv_cache must be [num_blocks, {H}, {17 * d}], got {tuple(shape)}")
+    return _arg("kv_cache", kv_cache, torch.uint8, None, dev), shape[0]
 
 
 def photon_kv_cache_write_fp4(k, v, positions, slot_mapping, kv_cache, rope_theta, rope_style="neox",
@@ -336,29 +363,27 @@ def photon_kv_cache_write_fp4(k, v, positions, slot_mapping, kv_cache, rope_thet
     """4-bit write: k, v [T, H_kv, d] (float32 or bfloat16); positions int32
     [T]; slot_mapping int64 [T]; kv_cache uint8 [num_blocks, H_kv, 17 * d]."""
     import torch
-    T, H, d = k.shape
-    nb = _fp4_pool(kv_cache, H, d)
-    _want("k", k, k.dtype)
-    _want("v", v, k.dtype, k.shape)
-    _want("positions", positions, torch.int32, (T,))
-    _want("slot_mapping", slot_mapping, torch.int64, (T,))
+    (T, H, d), dt = _rows("k", k)
+    dev = _device()
+    pool, nb = _pool(kv_cache, H, d, dev)
     style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
-    _check(lib().photon_kv_cache_write_fp4(_p(k), _p(v), _p(positions), _p(slot_mapping), _p(kv_cache), T, H,
-                                           d, 16, nb, _dt(k), float(rope_theta), style, _stream(stream)),
-           "photon_kv_cache_write_fp4")
+    _check(lib().photon_kv_cache_write_fp4(
+        _arg("k", k, k.dtype, None, dev), _arg("v", v, k.dtype, k.shape, dev),
+        _arg("positions", positions, torch.int32, (T,), dev),
+        _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), pool, T, H, d, 16, nb, dt, rope_theta, style,
+        _stream(stream)), "photon_kv_cache_write_fp4")
 
 
 def photon_kv_cache_read_fp4(kv_cache, slot_mapping, k, v, stream=None):
     """Dequantised rows of the tokens at slot_mapping (int64 [T]) into k and v
     [T, H_kv, d] (float32 or bfloat16)."""
     import torch
-    T, H, d = k.shape
-    nb = _fp4_pool(kv_cache, H, d)
-    _want("k", k, k.dtype)
-    _want("v", v, k.dtype, k.shape)
-    _want("slot_mapping", slot_mapping, torch.int64, (T,))
-    _check(lib().photon_kv_cache_read_fp4(_p(kv_cache), _p(slot_mapping), _p(k), _p(v), T, H, d, 16, nb, _dt(k),
-                                          _stream(stream)), "photon_kv_cache_read_fp4")
+    (T, H, d), dt = _rows("k", k)
+    dev = _device()
+    pool, nb = _pool(kv_cache, H, d, dev)
+    _check(lib().photon_kv_cache_read_fp4(
+        pool, _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), _arg("k", k, k.dtype, None, dev),
+        _arg("v", v, k.dtype, k.shape, dev), T, H, d, 16, nb, dt, _stream(stream)), "photon_kv_cache_read_fp4")
 
 
 def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
@@ -366,18 +391,20 @@ def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, s
     """Decode attention over a 4-bit pool (see photon_kv_cache_write_fp4); q
     bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
     import torch
-    B, Hq, d = q.shape
-    Hkv = kv_cache.shape[1]
-    nb = _fp4_pool(kv_cache, Hkv, d)
-    _want("q", q, torch.bfloat16)
-    _want("out", out, out.dtype, q.shape)
-    _want("block_tables", block_tables, torch.int32, (B, block_tables.shape[1]))
-    _want("context_lens", context_lens, torch.int32, (B,))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    (B, Hq, d), _ = _rows("q", q)
+    dev = _device()
+    Hkv, W = kv_cache.shape[1], block_tables.shape[1]
+    pool, nb = _pool(kv_cache, Hkv, d, dev)
+    if workspace is None:
+        ws, ws_bytes = None, 0
+    else:
+        ws = _arg("workspace", workspace, workspace.dtype, None, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib().photon_paged_attention_decode_fp4(
-        _p(q), _p(kv_cache), _p(block_tables), _p(context_lens), float(scale), _p(out), B, Hq, Hkv, d, 16, nb,
-        block_tables.shape[1], int(max_context_len), int(partition_size), _dt(out), _p(workspace), ws_bytes,
-        _stream(stream)), "photon_paged_attention_decode_fp4")
+        _arg("q", q, torch.bfloat16, None, dev), pool, _arg("block_tables", block_tables, torch.int32, (B, W), dev),
+        _arg("context_lens", context_lens, torch.int32, (B,), dev), scale, _arg("out", out, out.dtype, q.shape, dev),
+        B, Hq, Hkv, d, 16, nb, W, max_context_len, partition_size, _dt(out), ws, ws_bytes, _stream(stream)),
+        "photon_paged_attention_decode_fp4")
 
 
 def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block_tables, free_blocks, num_free,
@@ -392,21 +419,19 @@ def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block
     blocks, status)."""
     import torch
     B, W = block_tables.shape
-    M = token_seq.shape[0]
-    num_free_out = num_free if num_free_out is None else num_free_out
-    i32 = torch.int32
-    for what, t, shape in (("num_computed_tokens", num_computed_tokens, (B,)),
-                           ("num_new_tokens", num_new_tokens, (B,)), ("block_tables", block_tables, (B, W)),
-                           ("free_blocks", free_blocks, free_blocks.shape), ("num_free", num_free, (1,)),
-                           ("num_free_out", num_free_out, (1,)), ("token_seq", token_seq, (M,)),
-                           ("positions", positions, (M,)), ("context_lens", context_lens, (B,)),
-                           ("totals", totals, (4,))):
-        _want(what, t, i32, shape)
-    _want("slot_mapping", slot_mapping, torch.int64, (M,))
+    M, = token_seq.shape
+    blocks, = free_blocks.shape
+    i32, dev = torch.int32, _device()
+    free = _arg("num_free", num_free, i32, (1,), dev)
     _check(lib().photon_build_step_metadata_device(
-        _p(num_computed_tokens), _p(num_new_tokens), B, int(block_size), _p(block_tables), W, _p(free_blocks),
-        free_blocks.numel(), _p(num_free), _p(num_free_out), M, _p(token_seq), _p(positions),
-        _p(slot_mapping), _p(context_lens), _p(totals), _stream(stream)), "photon_build_step_metadata_device")
+        _arg("num_computed_tokens", num_computed_tokens, i32, (B,), dev),
+        _arg("num_new_tokens", num_new_tokens, i32, (B,), dev), B, block_size,
+        _arg("block_tables", block_tables, i32, None, dev), W, _arg("free_blocks", free_blocks, i32, None, dev),
+        blocks, free, free if num_free_out is None else _arg("num_free_out", num_free_out, i32, (1,), dev), M,
+        _arg("token_seq", token_seq, i32, None, dev), _arg("positions", positions, i32, (M,), dev),
+        _arg("slot_mapping", slot_mapping, torch.int64, (M,), dev),
+        _arg("context_lens", context_lens, i32, (B,), dev), _arg("totals", totals, i32, (4,), dev),
+        _stream(stream)), "photon_build_step_metadata_device")
 
 
 def photon_paged_attention_reduce(context_lens, out, max_context_len, partition_size=512,

@@ -59,7 +59,7 @@ struct Fp4WriteArgs {
   int32_t num_kv_heads;
   int32_t head_dim;
   int32_t rope_style;
-  int32_t tile;
+  int32_t tile_log2;
   unsigned long long turns[64];
 };
 

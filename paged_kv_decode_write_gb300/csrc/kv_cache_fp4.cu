@@ -94,14 +94,20 @@ __device__ __forceinline__ void two_prod(float a, float b, float &p, float &e) {
 
 // (cos hi, cos lo, sin hi, sin lo) of the fraction `turn` / 2^64 of a turn.
 __device__ __forceinline__ float4 cos_sin_turn(unsigned long long turn) {
-  const unsigned k = static_cast<unsigned>((turn + (1ull << 55)) >> 56) & 255u;
-  const long long rest = static_cast<long long>(turn - (static_cast<unsigned long long>(k) << 56));
-  const float4 a = *reinterpret_cast<const float4 *>(g_turn.v[k]);
-  // delta = 2 pi rest / 2^64 as dh + dl; rest has at most 56 bits
-  const float rh = __ll2float_rn(rest);
-  const float rl = __ll2float_rn(rest - static_cast<long long>(rh));
-  constexpr float kPiHi = static_cast<float>(kTurn * 0x1p-64);
-  constexpr float kPiLo = static_cast<float>(kTurn * 0x1p-64 - static_cast<double>(kPiHi));
+  const unsigned long long up = turn + (1ull << 55);
+  const float4 a = *reinterpret_cast<const float4 *>(g_turn.v[up >> 56]);
+  // rest = delta in units of 2^-64 turn, 56 bits: its leading 20 bits (signed)
+  // and the next 22 as exact floats through the mantissa (no conversion unit)
+  const unsigned hi = static_cast<unsigned>((up >> 24) & 0xffffffffu) ^ 0x80000000u;  // signed, 2^-40 turn
+  const unsigned lo = static_cast<unsigned>(up) & 0xffffffu;                            // 24 more bits
+  const float r1 = __uint_as_float(0x4b400000u + static_cast<unsigned>(static_cast<int>(hi) >> 12)) - 12582912.f;
+  const float r2 = __uint_as_float(0x4b000000u | ((hi & 0xfffu) << 10) | (lo >> 14)) - 8388608.f;
+  // in units of 2^-28 turn: rh + rl = r1 + r2 2^-22
+  const float rs = r2 * 0x1p-22f;
+  const float rh = __fadd_rn(r1, rs);
+  const float rl = __fsub_rn(rs, __fsub_rn(rh, r1));
+  constexpr float kPiHi = static_cast<float>(kTurn * 0x1p-28);
+  constexpr float kPiLo = static_cast<float>(kTurn * 0x1p-28 - static_cast<double>(kPiHi));
   float dh, de;
   two_prod(rh, kPiHi, dh, de);
   const float dl = de + fmaf(rh, kPiLo, rl * kPiHi);
@@ -212,12 +218,14 @@ __global__ void __launch_bounds__(kFp4Threads)
   using T = typename Tag::T;
   constexpr int LPR = D / 16;  // lanes of a row
   constexpr int HALF = D / 2;
-  __shared__ float4 cs[kFp4MaxTile][HALF];
+  // a token's (cos, sin) in the order its lanes read them: step i of lane w at
+  // i * LPR + w, rows padded so that a quarter warp's 16-byte reads meet no bank twice
+  __shared__ float4 cs[kFp4MaxTile][HALF + (D == 64 ? 4 : 0)];
   __shared__ int64_t slots[kFp4MaxTile];
   pdl_wait();
   pdl_launch_dependents();
   const int H = a.num_kv_heads;
-  const int t0 = blockIdx.x * a.tile, n = min(a.tile, a.num_tokens - t0);
+  const int t0 = blockIdx.x << a.tile_log2, tile = 1 << a.tile_log2, n = min(tile, a.num_tokens - t0);
   const bool rotate = a.rope_style != PHOTON_ROPE_NONE;
   const bool gptj = a.rope_style == PHOTON_ROPE_GPTJ;
   if (threadIdx.x < n) {
@@ -226,17 +234,21 @@ __global__ void __launch_bounds__(kFp4Threads)
     slots[threadIdx.x] = slot < a.num_slots ? slot : -1;
   }
   if (rotate)
-    for (int i = threadIdx.x; i < n * HALF; i += kFp4Threads)
-      cs[i / HALF][i % HALF] =
-          cos_sin_turn(static_cast<unsigned long long>(static_cast<long long>(a.positions[t0 + i / HALF])) *
-                       a.turns[i % HALF]);
+    for (int i = threadIdx.x; i < n * HALF; i += kFp4Threads) {
+      const int tt = i / HALF, pair = i % HALF;
+      // NEOX: lane w takes pairs 8w ..; GPT-J: 4w .. of either half
+      const int at = gptj ? (pair / (D / 4) * 4 + pair % 4) * LPR + pair % (D / 4) / 4 : pair % 8 * LPR + pair / 8;
+      cs[tt][at] = cos_sin_turn(
+          static_cast<unsigned long long>(static_cast<long long>(a.positions[t0 + tt])) * a.turns[pair]);
+    }
   __syncthreads();
   const int w = threadIdx.x % LPR;
-  const int rows = 2 * H * n;
+  const int rows = 2 * H * tile;
   // whole rows per warp: every lane of a row takes part in its shuffles
   for (int row = threadIdx.x / LPR; row - (threadIdx.x & 31) / LPR < rows; row += kFp4Threads / LPR) {
-    const bool in = row < rows;
-    const int tt = in ? row % n : 0, hv = in ? row / n : 0;
+    int tt = row & (tile - 1), hv = row >> a.tile_log2;
+    const bool in = row < rows && tt < n;
+    if (!in) tt = hv = 0;  // nothing to write: a row of its own to load
     const int v = hv >= H, h = hv - (v ? H : 0);  // K rows first
     const int64_t slot = slots[tt];
     const bool live = in && slot >= 0;
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kFp4Threads)
       if (gptj) {  // pairs (2i, 2i + 1): 4w .. 4w + 3, and D/4 + those in the upper half
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 p = cs[tt][4 * w + i], q = cs[tt][D / 4 + 4 * w + i];
+          const float4 p = cs[tt][i * LPR + w], q = cs[tt][(4 + i) * LPR + w];
           const float a0 = x0[2 * i], b0 = x0[2 * i + 1], a1 = x1[2 * i], b1 = x1[2 * i + 1];
           x0[2 * i] = stored(rotated(a0, b0, p.x, p.y, -p.z, -p.w), src);
           x0[2 * i + 1] = stored(rotated(b0, a0, p.x, p.y, p.z, p.w), src);
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kFp4Threads)
       } else {     // pairs (e, e + D/2)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 p = cs[tt][8 * w + i];
+          const float4 p = cs[tt][i * LPR + w];
           const float a0 = x0[i], b0 = x1[i];
           x0[i] = stored(rotated(a0, b0, p.x, p.y, -p.z, -p.w), src);
           x1[i] = stored(rotated(b0, a0, p.x, p.y, p.z, p.w), src);
@@ -279,8 +291,8 @@ __global__ void __launch_bounds__(kFp4Threads)
     }
     if (!live) continue;
     const uint32_t s0 = group_scale(m0), s1 = D > 64 ? group_scale(m1) : s0;
-    const int64_t blk = slot / kBlockSize;
-    const int r = static_cast<int>(slot - blk * kBlockSize);
+    const int64_t blk = slot >> 4;
+    const int r = static_cast<int>(slot) & (kBlockSize - 1);
     unsigned char *rec = static_cast<unsigned char *>(a.kv_cache) + (blk * H + h) * fp4_record_bytes(D);
     const int e0 = 8 * w, e1 = 8 * w + HALF;
     *reinterpret_cast<uint32_t *>(rec + (v ? fp4_v_byte(D, r, e0) : fp4_k_byte(r, e0))) = quant_word<Tag>(x0, s0);
@@ -307,73 +319,90 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
   *reinterpret_cast<uint4 *>(p) = w;
 }
 
-// One CTA per (16 consecutive tokens, KV head): tokens of one page then share
-// the sectors they read.  A lane takes one word of 8 dims of K or V per step,
-// all steps' loads in flight at once.
-constexpr int kFp4ReadTile = 16;
-
+// One CTA per (tile of consecutive tokens, KV head): tokens of one page then
+// share the sectors they read.  A lane takes the same 8 dims of a token's K and
+// V, so that the slot's arithmetic serves two words.
 template <typename Tag, int D>
 __global__ void __launch_bounds__(kFp4Threads)
-    kv_cache_read_fp4_kernel(const Fp4ReadArgs a, unsigned int *err) {
+    kv_cache_read_fp4_kernel(const Fp4ReadArgs a, int tile, unsigned int *err) {
   using T = typename Tag::T;
-  constexpr int WORDS = D / 4;                              // of K and V of a token and head
-  constexpr int STEPS = kFp4ReadTile * WORDS / kFp4Threads;  // 1 or 2
-  static_assert(STEPS * kFp4Threads == kFp4ReadTile * WORDS, "whole steps");
+  constexpr int LANES = D / 8;  // of a token
   pdl_wait();
   pdl_launch_dependents();
-  const int H = a.num_kv_heads;
-  const int tile = blockIdx.x / H, h = blockIdx.x - tile * H;
-  const int v = (threadIdx.x / (WORDS / 2)) & 1, e = 8 * (threadIdx.x % (WORDS / 2));
-  uint32_t code[STEPS], scale[STEPS];
-  int64_t row[STEPS];
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    const int64_t t = static_cast<int64_t>(tile) * kFp4ReadTile + (i * kFp4Threads + threadIdx.x) / WORDS;
-    row[i] = -1;
-    if (t >= a.num_tokens) continue;
-    const int64_t slot = a.slot_mapping[t];
-    if (slot < 0) continue;
-    if (slot >= a.num_slots) {
-      atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
+  const int H = a.num_kv_heads, h = blockIdx.x;
+  const int e = 8 * (threadIdx.x % LANES);
+  // a token's place in the record is a sum of a lane's part and a token's part
+  const unsigned char *base = static_cast<const unsigned char *>(a.pool) + static_cast<int64_t>(h) * fp4_record_bytes(D);
+  const int k_at = fp4_k_byte(0, e), v_at = fp4_v_byte(D, 0, e), s_at = fp4_scale_byte(D, 0, e / kFp4Group, 0);
+  const uint32_t block_bytes = static_cast<uint32_t>(H) * fp4_record_bytes(D);
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * tile;
+  const int left = static_cast<int>(min(static_cast<int64_t>(tile), a.num_tokens - first));
+  const int64_t *slots = a.slot_mapping + first;
+  const int64_t out_at = (first * H + h) * D + e;
+  T *k_out = static_cast<T *>(a.k_out) + out_at, *v_out = static_cast<T *>(a.v_out) + out_at;
+  const uint32_t out_step = static_cast<uint32_t>(H) * D;
+  for (int t = threadIdx.x / LANES; t < left; t += kFp4Threads / LANES) {
+    const int64_t slot = slots[t];
+    if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(a.num_slots)) {
+      if (slot >= 0) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
       continue;
     }
-    const int64_t blk = slot / kBlockSize;
-    const int r = static_cast<int>(slot - blk * kBlockSize);
-    const unsigned char *rec = static_cast<const unsigned char *>(a.pool) + (blk * H + h) * fp4_record_bytes(D);
-    code[i] = *reinterpret_cast<const uint32_t *>(rec + (v ? fp4_v_byte(D, r, e) : fp4_k_byte(r, e)));
-    scale[i] = *reinterpret_cast<const uint16_t *>(rec + fp4_scale_byte(D, r, e / kFp4Group, v));
-    row[i] = t * H + h;
-  }
+    const uint32_t quad = static_cast<uint32_t>(slot) >> 2 & 3u, odd = static_cast<uint32_t>(slot) & 1u,
+                   two = static_cast<uint32_t>(slot) & 2u;
+    const unsigned char *rec = base + static_cast<uint64_t>(static_cast<uint32_t>(slot >> 4)) * block_bytes;
+    const unsigned char *s = rec + (s_at + 16 * quad + 2 * odd + 2 * two);
+    const uint32_t code[2] = {*reinterpret_cast<const uint32_t *>(rec + (k_at + 128 * quad + 64 * odd + 4 * two)),
+                              *reinterpret_cast<const uint32_t *>(rec + (v_at + 16 * quad + 4 * odd + 4 * two))};
+    const uint32_t scale[2] = {*reinterpret_cast<const uint16_t *>(s), *reinterpret_cast<const uint16_t *>(s + 8)};
+    const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(t)) * out_step;
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    if (row[i] < 0) continue;
-    uint32_t f[4];
-    e2m1x8_to_f16(code[i], f);
-    const float s = bf16_bits_to_f32(scale[i]);
-    float x[8];
+    for (int v = 0; v < 2; ++v) {
+      uint32_t f[4];
+      e2m1x8_to_f16(code[v], f);
+      const float sc = bf16_bits_to_f32(scale[v]);
+      float x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&f[j]));
-      x[2 * j] = p.x * s;
-      x[2 * j + 1] = p.y * s;
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&f[j]));
+        x[2 * j] = p.x * sc;
+        x[2 * j + 1] = p.y * sc;
+      }
+      store8((v ? v_out : k_out) + row, x);
     }
-    store8(static_cast<T *>(v ? a.v_out : a.k_out) + row[i] * D + e, x);
   }
 }
 
 template <typename Tag>
 cudaError_t launch_write(const Fp4WriteArgs &a, unsigned int *err, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.num_tokens) + a.tile - 1) / a.tile));
+  const int64_t tile = int64_t{1} << a.tile_log2;
+  const dim3 grid(static_cast<unsigned>((a.num_tokens + tile - 1) / tile));
   auto kern = a.head_dim == 64 ? kv_cache_write_fp4_kernel<Tag, 64> : kv_cache_write_fp4_kernel<Tag, 128>;
   return launch_pdl(kern, grid, dim3(kFp4Threads), 0, st, a, err);
 }
 
 template <typename Tag>
 cudaError_t launch_read(const Fp4ReadArgs &a, unsigned int *err, cudaStream_t st) {
-  const int64_t tiles = (static_cast<int64_t>(a.num_tokens) + kFp4ReadTile - 1) / kFp4ReadTile;
-  if (tiles * a.num_kv_heads > INT32_MAX) return cudaErrorInvalidValue;
+  using T = typename Tag::T;
+  // 64 tokens per CTA where that leaves eight CTAs per SM, else 16
+  const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + 63) / 64 * a.num_kv_heads;
+  const int tile = ctas >= 8 * static_cast<int64_t>(device_sm_count()) ? 64 : 16;
+  const int64_t tiles = (static_cast<int64_t>(a.num_tokens) + tile - 1) / tile;
   auto kern = a.head_dim == 64 ? kv_cache_read_fp4_kernel<Tag, 64> : kv_cache_read_fp4_kernel<Tag, 128>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles * a.num_kv_heads)), dim3(kFp4Threads), 0, st, a, err);
+  // the grid's y extent is at most 65535 tiles: longer reads in pieces
+  constexpr int64_t kMaxTiles = 65535;
+  for (int64_t t = 0; t < tiles; t += kMaxTiles) {
+    Fp4ReadArgs p = a;
+    const int64_t first = t * tile, offset = first * a.num_kv_heads * a.head_dim;
+    p.slot_mapping = a.slot_mapping + first;
+    p.k_out = static_cast<T *>(a.k_out) + offset;
+    p.v_out = static_cast<T *>(a.v_out) + offset;
+    p.num_tokens = static_cast<int32_t>(a.num_tokens - first);
+    const int64_t y = tiles - t < kMaxTiles ? tiles - t : kMaxTiles;
+    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(a.num_kv_heads), static_cast<unsigned>(y)),
+                                     dim3(kFp4Threads), 0, st, p, tile, err);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -398,7 +427,7 @@ cudaError_t launch_kv_cache_write_fp4(const WriteArgs &wa, photon_dtype in_dt, u
   }
   // tokens per CTA: as many as leave two CTAs per SM
   const int64_t per = wa.num_tokens / (2 * static_cast<int64_t>(device_sm_count()));
-  a.tile = per >= 8 ? 8 : per >= 4 ? 4 : per >= 2 ? 2 : 1;
+  a.tile_log2 = per >= 8 ? 3 : per >= 4 ? 2 : per >= 2 ? 1 : 0;
   return in_dt == PHOTON_BF16 ? launch_write<BF16Tag>(a, err, st) : launch_write<F32Tag>(a, err, st);
 }
 
