@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(kFp4Threads)
   const int64_t out_at = (first * H + h) * D + e;
   T *k_out = static_cast<T *>(a.k_out) + out_at, *v_out = static_cast<T *>(a.v_out) + out_at;
   const uint32_t out_step = static_cast<uint32_t>(H) * D;
+#pragma unroll 1  // more loads in flight per lane measured slower (32768 tokens of d 128: 30.0 us, unrolled twice 33.3)
   for (int t = threadIdx.x / LANES; t < left; t += kFp4Threads / LANES) {
     const int64_t slot = slots[t];
     if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(a.num_slots)) {

@@ -32,7 +32,6 @@
 namespace photon {
 namespace {
 
-constexpr int kFp4Warps = 4;
 // Least exponent of the V scales that P follows: p is then at most 2^103 and
 // its sum over a context stays in fp32.
 constexpr int kFp4MinExp = -90;
@@ -85,19 +84,19 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 }
 
 // Stage ring of a warp: ST steps of PP pages, whole records.
-template <int D, int PP, int ST>
+template <int D, int PP, int ST, int NW>
 struct Fp4Ring {
   static constexpr int REC = fp4_record_bytes(D);
   static constexpr int STAGE = PP * REC;
-  static constexpr int SMEM = kFp4Warps * ST * (STAGE + 8);
+  static constexpr int SMEM = NW * ST * (STAGE + 8);
   static_assert(32 % PP == 0, "a step lies in one block-table window");
   static_assert(ST * PP <= 32, "a bit per page of the ring");
 };
 
-template <int D, int PP, int ST, int MIN_CTAS, bool BAL, bool SPLIT>
-__global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT>
+__global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     paged_decode_fp4_kernel(const DecodeArgs a, unsigned int *err) {
-  using R = Fp4Ring<D, PP, ST>;
+  using R = Fp4Ring<D, PP, ST, NW>;
   constexpr int HH = D / 64;
   constexpr int REC = R::REC;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
   const int g = lane >> 2, c = lane & 3;
   const int G = a.num_q_heads / a.num_kv_heads;
   unsigned char *stages = smem + warp * ST * R::STAGE;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kFp4Warps * ST * R::STAGE) + warp * ST;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NW * ST * R::STAGE) + warp * ST;
   if (lane == 0) {
     for (int i = 0; i < ST; ++i) mbar_init(&bars[i], 1);
     fence_mbar_init();
@@ -114,10 +113,10 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
   if constexpr (BAL) prefetch_tables_l2(a);
   pdl_launch_dependents();
   const uint64_t policy = l2_evict_first_policy();
-  const int total_warps = gridDim.x * kFp4Warps;
+  const int total_warps = gridDim.x * NW;
 
   Walker prod, w;  // the producer, ST steps ahead, and the consumer
-  walker_start<BAL>(prod, a, lane, err, blockIdx.x * kFp4Warps + warp, total_warps);
+  walker_start<BAL>(prod, a, lane, err, blockIdx.x * NW + warp, total_warps);
   w = prod;
   // metadata only so far; pages, q and the workspace wait for the preceding kernel
   pdl_wait();
@@ -430,10 +429,27 @@ __global__ void __launch_bounds__(kFp4Warps * 32, MIN_CTAS)
   }
 }
 
-template <int D, int PP, int ST, int MIN_CTAS, bool BAL, bool SPLIT>
-cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
-  constexpr int SMEM = Fp4Ring<D, PP, ST>::SMEM;
-  auto kern = paged_decode_fp4_kernel<D, PP, ST, MIN_CTAS, BAL, SPLIT>;
+// Long steps run one CTA of NW1 warps per SM, on steps of PP1 pages: the warp
+// scheduler shares an SM evenly between the warps of one CTA but prefers older
+// CTAs, and four CTAs of four warps with equal runs ended after 140, 158, 182
+// and 206 us (128 contexts of up to 32k tokens; kernel and merge 213 us, one
+// CTA of 16 warps 197 us, of 12 warps with steps of 8 pages 193 us; 32 of them
+// 59.9 -> 56.9 us; 64 of d 128 190.7 -> 176.2 us).  Chosen when the page bound
+// -- sequences x ceil(max context / 16) x KV heads -- reaches
+// kFp4MinPagesPerWarp per warp; ragged batches of some 30 pages per warp
+// (bounds of 120 to 140) lose 1 to 4 % with it, and grids smaller than the GPU
+// need CTAs of four warps to spread over its SMs.
+constexpr int64_t kFp4MinPagesPerWarp = 192;
+
+inline int64_t page_bound(const DecodeArgs &a) {
+  return static_cast<int64_t>(a.num_seqs) * ((static_cast<int64_t>(a.ctx_cap) + kBlockSize - 1) / kBlockSize) *
+         a.num_kv_heads;
+}
+
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT>
+cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *full) {
+  constexpr int SMEM = Fp4Ring<D, PP, ST, NW>::SMEM;
+  auto kern = paged_decode_fp4_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT>;
   static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -443,39 +459,44 @@ cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t
   if (occ == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kFp4Warps * 32, SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, NW * 32, SMEM);
     if (e != cudaSuccess) return e;
     occ = occ > 0 ? occ : 1;
     occupancy[dev].store(occ, std::memory_order_relaxed);
   }
   const int64_t items = static_cast<int64_t>(a.num_seqs) * a.max_partitions * a.num_kv_heads;
-  const int64_t warps_cap = static_cast<int64_t>(device_sm_count()) * occ * kFp4Warps;
+  const int64_t warps_cap = static_cast<int64_t>(device_sm_count()) * occ * NW;
+  if (full) {  // only for a full grid of long runs
+    *full = items >= warps_cap && page_bound(a) >= kFp4MinPagesPerWarp * warps_cap;
+    if (!*full) return cudaSuccess;
+  }
   const int64_t warps = items < warps_cap ? items : warps_cap;
-  const int grid = static_cast<int>((warps + kFp4Warps - 1) / kFp4Warps);
+  const int grid = static_cast<int>((warps + NW - 1) / NW);
   if (grid == 0) return cudaSuccess;
   DecodeArgs la = a;
   la.balanced = BAL ? 1 : 0;
-  return launch_pdl(kern, dim3(grid), dim3(kFp4Warps * 32), SMEM, stream, la, err);
+  return launch_pdl(kern, dim3(grid), dim3(NW * 32), SMEM, stream, la, err);
 }
 
-template <int D, int PP, int ST, int MIN_CTAS>
+template <int D, int PP, int ST, int MIN_CTAS, int PP1, int ST1, int NW1, bool SPLIT>
 cudaError_t launch_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
-  const bool bal = balanced_pieces(a);
-  if (a.out_bf16)
-    return bal ? launch_fp4_kern<D, PP, ST, MIN_CTAS, true, false>(a, err, stream)
-               : launch_fp4_kern<D, PP, ST, MIN_CTAS, false, false>(a, err, stream);
-  return bal ? launch_fp4_kern<D, PP, ST, MIN_CTAS, true, true>(a, err, stream)
-             : launch_fp4_kern<D, PP, ST, MIN_CTAS, false, true>(a, err, stream);
+  if (!balanced_pieces(a)) return launch_fp4_kern<D, PP, ST, 4, MIN_CTAS, false, SPLIT>(a, err, stream, nullptr);
+  bool full = false;
+  const cudaError_t e = launch_fp4_kern<D, PP1, ST1, NW1, 1, true, SPLIT>(a, err, stream, &full);
+  if (e != cudaSuccess || full) return e;
+  return launch_fp4_kern<D, PP, ST, 4, MIN_CTAS, true, SPLIT>(a, err, stream, nullptr);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
-  switch (a.head_dim) {
-    case 64: return launch_fp4<64, 4, 3, 4>(a, err, st);
-    case 128: return launch_fp4<128, 2, 3, 3>(a, err, st);
-    default: return cudaErrorInvalidValue;
-  }
+  if (a.head_dim == 64)
+    return a.out_bf16 ? launch_fp4<64, 4, 3, 4, 8, 2, 12, false>(a, err, st)
+                      : launch_fp4<64, 4, 3, 4, 8, 2, 12, true>(a, err, st);
+  if (a.head_dim == 128)
+    return a.out_bf16 ? launch_fp4<128, 2, 3, 3, 4, 2, 12, false>(a, err, st)
+                      : launch_fp4<128, 2, 3, 3, 4, 2, 12, true>(a, err, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace photon
