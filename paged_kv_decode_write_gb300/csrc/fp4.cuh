@@ -47,14 +47,16 @@ __device__ __forceinline__ int fp4_scale_byte(int d, int r, int hh, int v) {
   return 16 * d + 64 * hh + 16 * (r >> 2) + 8 * v + 2 * (r & 3);
 }
 
-// Two values -> their nearest E2M1 codes (halves to the even code, saturating
-// at +-6), lo in the low nibble.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+// Eight values -> their nearest E2M1 codes (halves to the even code, saturating
+// at +-6), value i in nibble i.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&y)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 p;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %1, %2;\n\t"
-      "mov.b32 %0, {p, 0, 0, 0};\n\t}"
+  asm("{\n\t.reg .b8 p0, p1, p2, p3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 p1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 p3, %8, %7;\n\t"
+      "mov.b32 %0, {p0, p1, p2, p3};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return r;
 }
 
@@ -65,16 +67,6 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&out)[4]) {
       "cvt.rn.f16x2.e2m1x2 %2, p2;\n\tcvt.rn.f16x2.e2m1x2 %3, p3;\n\t}"
       : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
       : "r"(w));
-}
-
-// The code pair in the low byte of b -> f16x2 (exact).
-__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t b) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 p0, p1, p2, p3;\n\tmov.b32 {p0, p1, p2, p3}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, p0;\n\t}"
-      : "=r"(r)
-      : "r"(b));
-  return r;
 }
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }

@@ -136,24 +136,59 @@ __device__ __forceinline__ float rotated(float u, float w, float ch, float cl, f
   return s + (se + (fmaf(u, cl, pe) + fmaf(w, tl, qe)));
 }
 
+__device__ __forceinline__ float stored(float v, float) { return v; }
+__device__ __forceinline__ float stored(float v, __nv_bfloat16) {
+  return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+// The 8 pairs of a lane, rotated and rounded to fp32 and then to the storage
+// type.  NEOX: (x0[i], x1[i]); GPT-J: (x0[2i], x0[2i + 1]), then those of x1.
+// cs: step i's entry at cs[i * stride].  (fp32 arithmetic first, with the
+// accurate sums only where an error bound leaves the bf16 rounding open, took
+// more registers and local memory: 30.5 -> 36.8 us for 16384 tokens.)
+template <typename T, bool GPTJ>
+__device__ __forceinline__ void rotate_lane(float (&x0)[8], float (&x1)[8], const float4 *cs, int stride) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float &u = GPTJ ? (i < 4 ? x0[2 * i] : x1[2 * i - 8]) : x0[i];
+    float &w = GPTJ ? (i < 4 ? x0[2 * i + 1] : x1[2 * i - 7]) : x1[i];
+    const float4 p = cs[i * stride];
+    const float a = u, b = w;
+    u = stored(rotated(a, b, p.x, p.y, -p.z, -p.w), T{});
+    w = stored(rotated(b, a, p.x, p.y, p.z, p.w), T{});
+  }
+}
+
 // ---- codes -----------------------------------------------------------------------
 
-// max that keeps a NaN of either operand
-__device__ __forceinline__ float max_nan(float a, float b) {
+// max |.| that keeps a NaN of any operand
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
-// Scale of a group whose largest magnitude is m (bf16 bits); a group that
-// holds an infinity or a NaN gets a NaN scale.
+// Scale of a group whose largest magnitude is m (bf16 bits): the quotient m / 6
+// rounded to fp32 (the product with 1/6 and one exact residual give it in the
+// normal range) and to bf16.  A group that holds an infinity or a NaN gets a
+// NaN scale.
 __device__ __forceinline__ uint32_t group_scale(float m) {
   if (!(m <= 3.4028234663852886e38f)) return 0x7fffu;
-  return __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(m, 6.f)));
+  constexpr float kSixth = 1.f / 6.f;
+  const float q0 = __fmul_rn(m, kSixth);
+  const float q = m < 0x1p-100f ? __fdiv_rn(m, 6.f) : __fmaf_rn(__fmaf_rn(-q0, 6.f, m), kSixth, q0);
+  return __bfloat16_as_ushort(__float2bfloat16_rn(q));
 }
 
-// x / s close enough for the code: y0 = x fl(1/s) corrected once by its exact
-// residual is the quotient when it has few bits, a midpoint of two codes among
+// 1 / s within an ulp (s normal, below 2^126).
+__device__ __forceinline__ float rcp_approx(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// x / s close enough for the code: y0 = x is, is the reciprocal within an ulp,
+// corrected once by its exact residual is the quotient when that has few bits, a midpoint of two codes among
 // them, and within an ulp otherwise.  A bf16 x (8 bits) over a bf16 s is never
 // within 2^-11 of a midpoint without being it; an fp32 x may be, and its y may
 // round onto the midpoint: the residual's sign then says which side it is on.
@@ -183,37 +218,50 @@ template <typename Tag>
 __device__ __forceinline__ uint32_t quant_word(const float (&x)[8], uint32_t sbits) {
   const float s = bf16_bits_to_f32(sbits);
   if (!(s > 0.f)) return 0u;  // an all-zero (or non-finite) group
-  uint32_t w = 0;
   if (s < 0x1p-100f) {
+    uint32_t w = 0;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) w |= code_by_midpoints(x[i], s) << (4 * i);
     return w;
   }
-  const float is = __frcp_rn(s);
+  const float is = rcp_approx(s);
+  float y[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= cvt_e2m1x2(quotient<Tag>(x[2 * i], s, is), quotient<Tag>(x[2 * i + 1], s, is)) << (8 * i);
-  return w;
+  for (int i = 0; i < 8; ++i) y[i] = quotient<Tag>(x[i], s, is);
+  return cvt_e2m1x8(y);
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  Unpack<BF16Tag>::run(*reinterpret_cast<const uint4 *>(p), x);
-}
-
-// fp32 value of v rounded to the storage type
-__device__ __forceinline__ float stored(float v, const float *) { return v; }
-__device__ __forceinline__ float stored(float v, const __nv_bfloat16 *) {
-  return __bfloat162float(__float2bfloat16_rn(v));
-}
+// A lane's 16 values of a row as loaded: dims 8w .. 8w + 7 and those + D/2.
+template <typename T>
+struct RowLoad {
+  static constexpr int N = sizeof(T) / 2;
+  uint4 lo[N], hi[N];
+  __device__ __forceinline__ void load(const T *src, int half) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      lo[i] = reinterpret_cast<const uint4 *>(src)[i];
+      hi[i] = reinterpret_cast<const uint4 *>(src + half)[i];
+    }
+  }
+  __device__ __forceinline__ static void widen(const uint4 (&r)[N], float (&x)[8]) {
+    if constexpr (N == 1) {
+      Unpack<BF16Tag>::run(r[0], x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[4 * i] = __uint_as_float(r[i].x);
+        x[4 * i + 1] = __uint_as_float(r[i].y);
+        x[4 * i + 2] = __uint_as_float(r[i].z);
+        x[4 * i + 3] = __uint_as_float(r[i].w);
+      }
+    }
+  }
+};
 
 // One CTA per tile of tokens (all heads): the tile's rotation table in shared
 // memory, then rows (K or V, head, token), token fastest, D/16 lanes each.
 template <typename Tag, int D>
-__global__ void __launch_bounds__(kFp4Threads)
+__global__ void __launch_bounds__(kFp4Threads, 4)
     kv_cache_write_fp4_kernel(const __grid_constant__ Fp4WriteArgs a, unsigned int *err) {
   using T = typename Tag::T;
   constexpr int LPR = D / 16;  // lanes of a row
@@ -221,18 +269,26 @@ __global__ void __launch_bounds__(kFp4Threads)
   // a token's (cos, sin) in the order its lanes read them: step i of lane w at
   // i * LPR + w, rows padded so that a quarter warp's 16-byte reads meet no bank twice
   __shared__ float4 cs[kFp4MaxTile][HALF + (D == 64 ? 4 : 0)];
-  __shared__ int64_t slots[kFp4MaxTile];
   pdl_wait();
   pdl_launch_dependents();
   const int H = a.num_kv_heads;
   const int t0 = blockIdx.x << a.tile_log2, tile = 1 << a.tile_log2, n = min(tile, a.num_tokens - t0);
   const bool rotate = a.rope_style != PHOTON_ROPE_NONE;
   const bool gptj = a.rope_style == PHOTON_ROPE_GPTJ;
-  if (threadIdx.x < n) {
-    const int64_t slot = a.slot_mapping[t0 + threadIdx.x];
-    if (slot >= a.num_slots) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
-    slots[threadIdx.x] = slot < a.num_slots ? slot : -1;
-  }
+  // a lane keeps its token; its first row is on the way while the table is made
+  const int w = threadIdx.x % LPR, row = threadIdx.x / LPR;
+  const int tt = min(row & (tile - 1), n - 1);  // past the last token: its rows again, not written
+  const int64_t token = static_cast<int64_t>(t0 + tt) * H * D + 8 * w;
+  const T *k_src = static_cast<const T *>(a.k) + token, *v_src = static_cast<const T *>(a.v) + token;
+  const int first = row >> a.tile_log2, step = (kFp4Threads / LPR) >> a.tile_log2;
+  // rows: K of every head, then V; the same number of turns for every lane
+  auto source = [&](int hv) -> const T * {
+    hv = min(hv, 2 * H - 1);
+    return hv >= H ? v_src + (hv - H) * D : k_src + hv * D;
+  };
+  RowLoad<T> next;
+  next.load(source(first), HALF);
+  const int64_t slot_in = a.slot_mapping[t0 + tt];
   if (rotate)
     for (int i = threadIdx.x; i < n * HALF; i += kFp4Threads) {
       const int tt = i / HALF, pair = i % HALF;
@@ -242,63 +298,53 @@ __global__ void __launch_bounds__(kFp4Threads)
           static_cast<unsigned long long>(static_cast<long long>(a.positions[t0 + tt])) * a.turns[pair]);
     }
   __syncthreads();
-  const int w = threadIdx.x % LPR;
-  const int rows = 2 * H * tile;
-  // whole rows per warp: every lane of a row takes part in its shuffles
-  for (int row = threadIdx.x / LPR; row - (threadIdx.x & 31) / LPR < rows; row += kFp4Threads / LPR) {
-    int tt = row & (tile - 1), hv = row >> a.tile_log2;
-    const bool in = row < rows && tt < n;
-    if (!in) tt = hv = 0;  // nothing to write: a row of its own to load
-    const int v = hv >= H, h = hv - (v ? H : 0);  // K rows first
-    const int64_t slot = slots[tt];
-    const bool live = in && slot >= 0;
-    const T *src = static_cast<const T *>(v ? a.v : a.k) + (static_cast<int64_t>(t0 + tt) * H + h) * D + 8 * w;
+  if (slot_in >= a.num_slots && w == 0) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
+  const bool live = (row & (tile - 1)) < n && slot_in >= 0 && slot_in < a.num_slots;
+  const int64_t slot = live ? slot_in : 0;
+  const int r = static_cast<int>(slot) & (kBlockSize - 1);
+  const int e0 = 8 * w, e1 = 8 * w + HALF;
+  const int k_at[2] = {fp4_k_byte(r, e0), fp4_k_byte(r, e1)};
+  const int v_at[2] = {fp4_v_byte(D, r, e0), fp4_v_byte(D, r, e1)};
+  const int s_at = fp4_scale_byte(D, r, w < D / kFp4Group ? w : 0, 0);
+  unsigned char *block = static_cast<unsigned char *>(a.kv_cache) +
+                         (slot >> 4) * (static_cast<int64_t>(H) * fp4_record_bytes(D));
+  for (int base = 0; base < 2 * H; base += step) {
+    const int hv = min(base + first, 2 * H - 1);
+    const bool in = base + first < 2 * H;
+    const int v = hv >= H, h = hv - (v ? H : 0);
     float x0[8], x1[8];
-    load8(src, x0);
-    load8(src + HALF, x1);
+    RowLoad<T>::widen(next.lo, x0);
+    RowLoad<T>::widen(next.hi, x1);
+    if (base + step < 2 * H) next.load(source(base + step + first), HALF);
     if (rotate && !v) {
-      if (gptj) {  // pairs (2i, 2i + 1): 4w .. 4w + 3, and D/4 + those in the upper half
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 p = cs[tt][i * LPR + w], q = cs[tt][(4 + i) * LPR + w];
-          const float a0 = x0[2 * i], b0 = x0[2 * i + 1], a1 = x1[2 * i], b1 = x1[2 * i + 1];
-          x0[2 * i] = stored(rotated(a0, b0, p.x, p.y, -p.z, -p.w), src);
-          x0[2 * i + 1] = stored(rotated(b0, a0, p.x, p.y, p.z, p.w), src);
-          x1[2 * i] = stored(rotated(a1, b1, q.x, q.y, -q.z, -q.w), src);
-          x1[2 * i + 1] = stored(rotated(b1, a1, q.x, q.y, q.z, q.w), src);
-        }
-      } else {     // pairs (e, e + D/2)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 p = cs[tt][i * LPR + w];
-          const float a0 = x0[i], b0 = x1[i];
-          x0[i] = stored(rotated(a0, b0, p.x, p.y, -p.z, -p.w), src);
-          x1[i] = stored(rotated(b0, a0, p.x, p.y, p.z, p.w), src);
-        }
-      }
+      if (gptj)
+        rotate_lane<T, true>(x0, x1, cs[tt] + w, LPR);
+      else
+        rotate_lane<T, false>(x0, x1, cs[tt] + w, LPR);
     }
-    float m0 = fabsf(x0[0]), m1 = fabsf(x1[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      m0 = max_nan(m0, fabsf(x0[i]));
-      m1 = max_nan(m1, fabsf(x1[i]));
+    // the largest magnitude of each group: at D = 64 one of all dims, at D = 128
+    // one of x0 and one of x1
+    float m0 = max_abs(x0[0], x0[1], x0[2]), m1 = max_abs(x1[0], x1[1], x1[2]);
+    m0 = max_abs(max_abs(m0, x0[3], x0[4]), x0[5], x0[6]);
+    m1 = max_abs(max_abs(m1, x1[3], x1[4]), x1[5], x1[6]);
+    if (D == 64) {
+      m0 = max_abs(max_abs(m0, m1, x0[7]), x1[7], 0.f);
+    } else {
+      m0 = max_abs(m0, x0[7], 0.f);
+      m1 = max_abs(m1, x1[7], 0.f);
     }
-    if (D == 64) m0 = max_nan(m0, m1);  // one group of 64 dims; at D = 128 x0 and x1 are one each
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) {
-      m0 = max_nan(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-      if (D > 64) m1 = max_nan(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+      m0 = max_abs(m0, __shfl_xor_sync(0xffffffffu, m0, o), 0.f);
+      if (D > 64) m1 = max_abs(m1, __shfl_xor_sync(0xffffffffu, m1, o), 0.f);
     }
-    if (!live) continue;
+    if (!live || !in) continue;
     const uint32_t s0 = group_scale(m0), s1 = D > 64 ? group_scale(m1) : s0;
-    const int64_t blk = slot >> 4;
-    const int r = static_cast<int>(slot) & (kBlockSize - 1);
-    unsigned char *rec = static_cast<unsigned char *>(a.kv_cache) + (blk * H + h) * fp4_record_bytes(D);
-    const int e0 = 8 * w, e1 = 8 * w + HALF;
-    *reinterpret_cast<uint32_t *>(rec + (v ? fp4_v_byte(D, r, e0) : fp4_k_byte(r, e0))) = quant_word<Tag>(x0, s0);
-    *reinterpret_cast<uint32_t *>(rec + (v ? fp4_v_byte(D, r, e1) : fp4_k_byte(r, e1))) = quant_word<Tag>(x1, s1);
+    unsigned char *rec = block + h * fp4_record_bytes(D);
+    *reinterpret_cast<uint32_t *>(rec + (v ? v_at[0] : k_at[0])) = quant_word<Tag>(x0, s0);
+    *reinterpret_cast<uint32_t *>(rec + (v ? v_at[1] : k_at[1])) = quant_word<Tag>(x1, s1);
     if (w < D / kFp4Group)
-      *reinterpret_cast<uint16_t *>(rec + fp4_scale_byte(D, r, w, v)) = static_cast<uint16_t>(w ? s1 : s0);
+      *reinterpret_cast<uint16_t *>(rec + s_at + 8 * v) = static_cast<uint16_t>(w ? s1 : s0);
   }
 }
 
@@ -426,7 +472,8 @@ cudaError_t launch_kv_cache_write_fp4(const WriteArgs &wa, photon_dtype in_dt, u
     const double x = wa.inv_freq[i] / kTurn;
     a.turns[i] = static_cast<unsigned long long>(std::ldexp(x - std::floor(x), 64));
   }
-  // tokens per CTA: as many as leave two CTAs per SM
+  // tokens per CTA: up to 8, as many as leave two CTAs per SM (16384 tokens written
+  // and read back: 24.1 us, 26.7 with four each)
   const int64_t per = wa.num_tokens / (2 * static_cast<int64_t>(device_sm_count()));
   a.tile_log2 = per >= 8 ? 3 : per >= 4 ? 2 : per >= 2 ? 1 : 0;
   return in_dt == PHOTON_BF16 ? launch_write<BF16Tag>(a, err, st) : launch_write<F32Tag>(a, err, st);

@@ -491,8 +491,8 @@ cudaError_t launch_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t stre
 
 cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
   if (a.head_dim == 64)
-    return a.out_bf16 ? launch_fp4<64, 4, 3, 4, 8, 2, 12, false>(a, err, st)
-                      : launch_fp4<64, 4, 3, 4, 8, 2, 12, true>(a, err, st);
+    return a.out_bf16 ? launch_fp4<64, 2, 5, 4, 8, 2, 12, false>(a, err, st)
+                      : launch_fp4<64, 2, 5, 4, 8, 2, 12, true>(a, err, st);
   if (a.head_dim == 128)
     return a.out_bf16 ? launch_fp4<128, 2, 3, 3, 4, 2, 12, false>(a, err, st)
                       : launch_fp4<128, 2, 3, 3, 4, 2, 12, true>(a, err, st);

@@ -610,8 +610,13 @@ int photon_kv_cache_write_fp4(const void *k, const void *v, const int32_t *posit
   a.num_kv_heads = num_kv_heads;
   a.head_dim = head_dim;
   a.rope_style = rope_style;
-  for (int i = 0; i < head_dim / 2; ++i)
-    a.inv_freq[i] = std::pow(static_cast<double>(rope_theta), -2.0 * i / head_dim);
+  // theta^(-2 (8 j + k) / d) as a product of two powers: 12 or 16 of them, not 32 or 64 (1 us of the call)
+  double fine[8];
+  for (int k = 0; k < 8; ++k) fine[k] = std::pow(static_cast<double>(rope_theta), -2.0 * k / head_dim);
+  for (int j = 0; j < head_dim / 16; ++j) {
+    const double coarse = std::pow(static_cast<double>(rope_theta), -16.0 * j / head_dim);
+    for (int k = 0; k < 8; ++k) a.inv_freq[8 * j + k] = coarse * fine[k];
+  }
   unsigned int *err = error_word();
   if (!err) return PHOTON_ERR_CUDA;
   return cuda_status(launch_kv_cache_write_fp4(a, in_dtype, err, reinterpret_cast<cudaStream_t>(stream)));
