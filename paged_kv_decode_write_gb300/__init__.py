@@ -159,20 +159,27 @@ def _p(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-_raw_stream = None  # device index -> handle of its current stream
+_raw = None  # (current device's index, device index -> handle of its current stream)
+
+
+def _raw_getters():
+    """torch's raw getters: a Stream object for the current stream costs 3 us
+    of a call's 10, and the checks around current_device() another half."""
+    global _raw
+    if _raw is None:
+        import torch
+        _raw = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                getattr(torch._C, "_cuda_getCurrentRawStream",
+                        lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    return _raw
 
 
 def _stream(stream):
-    """Handle of the given stream, or of the current one (torch's raw getter:
-    building a Stream object for it costs 3 us of a call's 10)."""
-    global _raw_stream
+    """Handle of the given stream, or of the current device's current one."""
     if stream is not None:
         return stream.cuda_stream
     import torch
-    if _raw_stream is None:
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_getters()[1](torch.cuda.current_device())
 
 
 def photon_kv_cache_write(k, v, positions, slot_mapping, k_cache, v_cache, rope_theta,
@@ -337,10 +344,13 @@ def _arg(what, t, dtype, shape, dev):
     return t.data_ptr()
 
 
-def _device():
-    """The current CUDA device's index (no tensor is on it, -2, without one)."""
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+def _place(what, t, stream):
+    """(device, stream handle) of a call on the current device, which t must be on."""
+    device, raw_stream = _raw_getters()
+    dev = t.get_device()
+    if dev < 0 or dev != device():
+        raise ValueError(f"{what} must be on the current CUDA device, got {t.device}")
+    return dev, raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _rows(what, t):
@@ -364,14 +374,14 @@ def photon_kv_cache_write_fp4(k, v, positions, slot_mapping, kv_cache, rope_thet
     [T]; slot_mapping int64 [T]; kv_cache uint8 [num_blocks, H_kv, 17 * d]."""
     import torch
     (T, H, d), dt = _rows("k", k)
-    dev = _device()
+    dev, st = _place("k", k, stream)
     pool, nb = _pool(kv_cache, H, d, dev)
     style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
     _check(lib().photon_kv_cache_write_fp4(
         _arg("k", k, k.dtype, None, dev), _arg("v", v, k.dtype, k.shape, dev),
         _arg("positions", positions, torch.int32, (T,), dev),
-        _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), pool, T, H, d, 16, nb, dt, rope_theta, style,
-        _stream(stream)), "photon_kv_cache_write_fp4")
+        _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), pool, T, H, d, 16, nb, dt, float(rope_theta),
+        style, st), "photon_kv_cache_write_fp4")
 
 
 def photon_kv_cache_read_fp4(kv_cache, slot_mapping, k, v, stream=None):
@@ -379,11 +389,11 @@ def photon_kv_cache_read_fp4(kv_cache, slot_mapping, k, v, stream=None):
     [T, H_kv, d] (float32 or bfloat16)."""
     import torch
     (T, H, d), dt = _rows("k", k)
-    dev = _device()
+    dev, st = _place("k", k, stream)
     pool, nb = _pool(kv_cache, H, d, dev)
     _check(lib().photon_kv_cache_read_fp4(
         pool, _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), _arg("k", k, k.dtype, None, dev),
-        _arg("v", v, k.dtype, k.shape, dev), T, H, d, 16, nb, dt, _stream(stream)), "photon_kv_cache_read_fp4")
+        _arg("v", v, k.dtype, k.shape, dev), T, H, d, 16, nb, dt, st), "photon_kv_cache_read_fp4")
 
 
 def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
@@ -392,7 +402,7 @@ def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, s
     bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
     import torch
     (B, Hq, d), _ = _rows("q", q)
-    dev = _device()
+    dev, st = _place("q", q, stream)
     Hkv, W = kv_cache.shape[1], block_tables.shape[1]
     pool, nb = _pool(kv_cache, Hkv, d, dev)
     if workspace is None:
@@ -402,8 +412,8 @@ def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, s
         ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib().photon_paged_attention_decode_fp4(
         _arg("q", q, torch.bfloat16, None, dev), pool, _arg("block_tables", block_tables, torch.int32, (B, W), dev),
-        _arg("context_lens", context_lens, torch.int32, (B,), dev), scale, _arg("out", out, out.dtype, q.shape, dev),
-        B, Hq, Hkv, d, 16, nb, W, max_context_len, partition_size, _dt(out), ws, ws_bytes, _stream(stream)),
+        _arg("context_lens", context_lens, torch.int32, (B,), dev), float(scale), _arg("out", out, out.dtype, q.shape, dev),
+        B, Hq, Hkv, d, 16, nb, W, int(max_context_len), int(partition_size), _dt(out), ws, ws_bytes, st),
         "photon_paged_attention_decode_fp4")
 
 
@@ -421,17 +431,18 @@ def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block
     B, W = block_tables.shape
     M, = token_seq.shape
     blocks, = free_blocks.shape
-    i32, dev = torch.int32, _device()
+    i32 = torch.int32
+    dev, st = _place("block_tables", block_tables, stream)
     free = _arg("num_free", num_free, i32, (1,), dev)
     _check(lib().photon_build_step_metadata_device(
         _arg("num_computed_tokens", num_computed_tokens, i32, (B,), dev),
-        _arg("num_new_tokens", num_new_tokens, i32, (B,), dev), B, block_size,
+        _arg("num_new_tokens", num_new_tokens, i32, (B,), dev), B, int(block_size),
         _arg("block_tables", block_tables, i32, None, dev), W, _arg("free_blocks", free_blocks, i32, None, dev),
         blocks, free, free if num_free_out is None else _arg("num_free_out", num_free_out, i32, (1,), dev), M,
         _arg("token_seq", token_seq, i32, None, dev), _arg("positions", positions, i32, (M,), dev),
         _arg("slot_mapping", slot_mapping, torch.int64, (M,), dev),
         _arg("context_lens", context_lens, i32, (B,), dev), _arg("totals", totals, i32, (4,), dev),
-        _stream(stream)), "photon_build_step_metadata_device")
+        st), "photon_build_step_metadata_device")
 
 
 def photon_paged_attention_reduce(context_lens, out, max_context_len, partition_size=512,

@@ -654,6 +654,7 @@ int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const
   if (rc != PHOTON_OK) return rc;
   rc = photon::check_fp4_pool(num_kv_heads, head_dim, block_size, num_blocks);
   if (rc != PHOTON_OK || num_seqs == 0) return rc;
+  if (max_context_len > INT32_MAX - 1024) return PHOTON_ERR_UNSUPPORTED;  // a step's tokens past the end stay int32
   unsigned int *err = error_word();
   if (!err) return PHOTON_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -111,6 +111,52 @@ def test_write_codes_equal_the_oracle(T, H, style, dtype, d):
     assert pk.photon_device_errors() == (pk.DEVERR_SLOT_RANGE if (gpu_slots >= nb * 16).any() else 0)
 
 
+@pytest.mark.parametrize("T,H,d", [(5003, 1, 64), (1301, 2, 128), (700, 3, 64)])
+def test_write_of_long_batches_equals_the_oracle(T, H, d):
+    """Tiles of several tokens per CTA with a ragged end, skipped and
+    out-of-pool slots among them; untouched bytes as they were."""
+    pk = ensure_built()
+    rng = np.random.default_rng(T)
+    nb = T // 16 + 5
+    k, kt = _storage(rng.standard_normal((T, H, d)), "bf16")
+    v, vt = _storage(rng.standard_normal((T, H, d)) * 3, "bf16")
+    slots = rng.permutation(nb * 16)[:T].astype(np.int64)
+    slots[::17] = -1
+    gpu_slots = slots.copy()
+    gpu_slots[17] = nb * 16 + 5
+    pos = rng.integers(0, 2 ** 20, T).astype(np.int32)
+    want = rng.integers(0, 256, (nb, H, 17 * d), dtype=np.uint8)
+    pool = _dev(want.copy())
+    pk.photon_device_errors()
+    pk.photon_kv_cache_write_fp4(kt, vt, _dev(pos), _dev(gpu_slots), pool, 1e6)
+    fp4.write(k, v, pos, slots, want, 1e6)
+    assert np.array_equal(pool.cpu().numpy(), want)
+    assert pk.photon_device_errors() == pk.DEVERR_SLOT_RANGE
+
+
+@pytest.mark.parametrize("style", ["neox", "gptj"])
+def test_write_rotates_infinities_and_nans_into_nan_groups(style):
+    """A pair that holds an infinity or a NaN makes the groups of both its
+    dims NaN, at position 0 too; the row's other group is as without it."""
+    pk = ensure_built()
+    rng = np.random.default_rng(3)
+    d, T = 128, 4
+    x = rng.standard_normal((T, 1, d)).astype(np.float32)
+    x[1, 0, 3], x[2, 0, 3], x[3, 0, 70] = np.inf, np.nan, -np.inf
+    pos = np.array([5, 0, 1000, 17], np.int32)
+    pool = _dev(np.zeros((1, 1, 17 * d), np.uint8))
+    _, xt = _storage(x, "bf16")
+    pk.photon_kv_cache_write_fp4(xt, xt, _dev(pos), _dev(np.arange(T, dtype=np.int64)), pool, 1e4, style)
+    kd, vd = fp4.dequant(pool.cpu().numpy(), d)
+    nan = np.isnan(kd[0, 0, :T]).reshape(T, 2, 64).all(-1)
+    fine = np.isfinite(kd[0, 0, :T]).reshape(T, 2, 64).all(-1)
+    both = style == "neox"                                  # dims 3 and 67 are a pair
+    assert nan.tolist() == [[False, False], [True, both], [True, both], [both, True]]
+    assert np.array_equal(fine, ~nan)
+    assert np.isnan(vd[0, 0, :T]).reshape(T, 2, 64).all(-1).tolist() == [[False, False], [True, False],
+                                                                       [True, False], [False, True]]
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_write_midpoints_and_special_groups(d):
     """fp32 rows whose quotient by the group's scale is exactly a midpoint, or
@@ -176,6 +222,21 @@ def test_read_returns_the_rounded_values(T, H, dtype, d):
         want = torch.from_numpy(np.where(skip[:, None, None], -3.0, want)).float().to(dt)
         assert torch.equal(got.cpu(), want)
     assert pk.photon_device_errors() == (pk.DEVERR_SLOT_RANGE if (slots >= nb * 16).any() else 0)
+
+
+def test_read_longer_than_one_grid():
+    """More tokens than one launch's tiles: every row, at its own place."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(9)
+    d, nb, T = 64, 3, 64 * 65535 + 77
+    pool = _random_pool(rng, nb, 1, d)
+    slots = torch.randint(0, nb * 16, (T,), generator=torch.Generator().manual_seed(1)).cuda()
+    k, v = (torch.empty(T, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pk.photon_kv_cache_read_fp4(_dev(pool), slots, k, v)
+    for got, val in zip((k, v), fp4.dequant(pool, d)):
+        rows = torch.from_numpy(val[:, 0].reshape(nb * 16, d)).float().bfloat16().cuda()
+        assert torch.equal(got[:, 0], rows[slots])
 
 
 CONTEXTS = [([1, 17, 600, 1500, 33, 0], 256), ([3000, 9, 700, 0, 16], 512),
@@ -358,6 +419,73 @@ def test_decode_of_full_grids(H, G, d, kind):
     tol = _tolerance(oracle.to_f64(q), kd, vd, ctx, d ** -0.5, False, ref)
     assert (np.abs(a.double().cpu().numpy() - ref) <= tol).all()
     assert pk.photon_device_errors() == 0
+
+
+@pytest.mark.parametrize("G,d,H", [(4, 64, 8), (1, 64, 8), (2, 128, 8), (8, 128, 16)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_decode_declared_long(G, d, H, out):
+    """A batch whose declared bound asks for the long steps' kernel (192 pages
+    per warp and more), the contexts themselves short, ragged, empty or long;
+    garbage behind each, and a bad block id."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(G + d)
+    ctx = [3001, 0, 1, 129, 128, 127, 16, 700]
+    width = -(-192 * 16 * 160 // (len(ctx) * H)) + 1
+    nb = sum(-(-c // 16) for c in ctx) + 2
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb, width=width)
+    bt[:, 200:] = 7                                       # past every context: never read
+    q, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    clean = pool.copy()
+    byte, nib, sb = fp4.record_positions(d)
+    for s, c in enumerate(ctx):
+        for r in range(c % 16, 16 if c % 16 else 0):
+            for w in range(2):
+                pool[bt[s, c // 16]][:, sb[w, r]] = 0x80
+                pool[bt[s, c // 16]][:, sb[w, r] + 1] = 0x7F
+    pk.photon_device_errors()
+    got = _decode(pk, qt, _dev(pool), bt, ctx, d ** -0.5, dt, 64, max_ctx=width * 16)
+    assert torch.equal(got, _decode(pk, qt, _dev(pool), bt, ctx, d ** -0.5, dt, 64, max_ctx=width * 16))
+    ref = fp4.paged_attention(q, clean, bt, ctx, d ** -0.5)
+    kd, vd = fp4.dequant(clean, d)
+    tol = _tolerance(oracle.to_f64(q), kd, vd, ctx, d ** -0.5, out == "bf16", ref)
+    assert (np.abs(got.double().cpu().numpy() - ref) <= tol).all()
+    assert pk.photon_device_errors() == 0
+    bt[3, 2] = -3
+    again = _decode(pk, qt, _dev(pool), bt, ctx, d ** -0.5, dt, 64, max_ctx=width * 16)
+    rows = [s for s in range(len(ctx)) if s != 3]
+    assert torch.equal(again[rows], got[rows]) and torch.isfinite(again).all()
+    assert pk.photon_device_errors() == pk.DEVERR_BLOCK_RANGE
+
+
+def test_decode_on_another_stream_and_two_at_once():
+    """Two decodes on two streams, each with its own workspace: the results of
+    one after the other."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(4)
+    ctx = [int(x) for x in rng.integers(1, 3000, 24)]
+    nb = sum(-(-c // 16) for c in ctx)
+    pool, bt = _dev(_random_pool(rng, nb, 4, 64)), _dev(_tables(rng, ctx, nb))
+    cl = _dev(np.array(ctx, np.int32))
+    _, qa = _storage(rng.standard_normal((24, 16, 64)), "bf16")
+    _, qb = _storage(rng.standard_normal((24, 16, 64)), "bf16")
+    n = pk.photon_paged_attention_workspace_size(24, 16, 64, max(ctx), 64)
+    ws = [torch.randint(0, 256, (n,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.empty(24, 16, 64, device="cuda") for _ in range(4)]
+    args = lambda q, i: (q, pool, bt, cl, 0.125, outs[i], max(ctx), 64, ws[i & 1])
+    pk.photon_paged_attention_decode_fp4(*args(qa, 0))
+    pk.photon_paged_attention_decode_fp4(*args(qb, 1))
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        pk.photon_paged_attention_decode_fp4(*args(qa, 2), stream=sa)
+        with torch.cuda.stream(sb):
+            pk.photon_paged_attention_decode_fp4(*args(qb, 3))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
 def test_decode_repeats_bit_for_bit():

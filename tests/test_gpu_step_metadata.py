@@ -202,14 +202,15 @@ def test_count_may_go_to_another_buffer():
         assert dev.tables.tolist() == [[0, 1, 2, -1]]
 
 
-def test_captured_decode_steps_over_the_4_bit_cache():
+@pytest.mark.parametrize("M", [64, 5000])
+def test_captured_decode_steps_over_the_4_bit_cache(M):
     """A whole step (metadata, 4-bit write, decode) captured once and replayed,
     the lengths advanced on the GPU: each step's output against the oracle on
     the pool's own codes, prompts admitted and a request released on the way."""
     torch = _torch()
     pk = ensure_built()
     rng = np.random.default_rng(11)
-    B, W, H, G, d, nb, M = 4, 8, 2, 4, 64, 40, 64
+    B, W, H, G, d, nb = 4, 8, 2, 4, 64, 40
     i32 = dict(dtype=torch.int32, device="cuda")
     nc, nn = torch.zeros(B, **i32), torch.zeros(B, **i32)
     k = torch.empty(M, H, d, dtype=torch.bfloat16, device="cuda")
