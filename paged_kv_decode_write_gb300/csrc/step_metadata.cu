@@ -12,7 +12,7 @@
 // released blocks), a binary search in shared memory naming the sequence, so
 // long prompts and thousands of one-token sequences cost the same per entry.
 //
-// One cluster of up to eight CTAs: every CTA computes all sums itself (reading
+// One cluster of up to sixteen CTAs: every CTA computes all sums itself (reading
 // 8 bytes per sequence) and takes its share of the flat loops, so the only
 // exchange is one cluster barrier between the pushes onto the stack and the
 // reads from it.  The loops' searches and loads are latency, not bandwidth:
@@ -20,6 +20,7 @@
 //
 // The kernel never lets a dependent grid start early: the decode kernels read
 // block tables and context lengths before their own dependency wait.
+#include <atomic>
 #include <climits>
 
 #include "common.cuh"
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kMetaThreads = 1024;
 
-constexpr int kMetaMaxCtas = 8;   // portable cluster size
+constexpr int kMetaMaxCtas = 16;  // of a cluster; 8 where the GPU has no room for one of 16
 constexpr int kMetaBatch = 4;
 
 // The last index s in [0, n) with off[s] <= x (off ascending, off[0] <= x).
@@ -184,13 +185,17 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
       a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + have + (j - gro[s])] = __ldcg(top - j);
     }
 
-  // ---- tokens, a span of 32 N neighbours per warp
-  for (int64_t base = static_cast<int64_t>(gtid >> 5) * (32 * N); base < T; base += static_cast<int64_t>(threads) * N) {
+  // ---- tokens, a span of up to 32 N neighbours per warp
+  const int turns = min(N, (T + threads - 1) / threads);
+  for (int64_t base = static_cast<int64_t>(gtid >> 5) * (32 * turns); base < T;
+       base += static_cast<int64_t>(threads) * turns) {
     int x[N], s[N], nc[N], p[N];
     int from = owner(tok, B, static_cast<int>(base));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       x[i] = static_cast<int>(min(base + 32 * i + lane, static_cast<int64_t>(T - 1)));
+      s[i] = from;
+      if (i >= turns) continue;
       s[i] = warp_owner(tok, B, x[i], from, lane);
       from = __shfl_sync(0xffffffffu, s[i], 31);
     }
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int64_t t = base + 32 * i + lane;
-      if (t >= T) continue;
+      if (i >= turns || t >= T) continue;
       const bool valid = id[i] >= 0 && id[i] < a.num_blocks;
       if (!valid) atomicOr(err, PHOTON_DEVERR_BLOCK_RANGE);
       a.token_seq[t] = s[i];
@@ -239,19 +244,54 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
 
 }  // namespace
 
+namespace {
+
+// The largest cluster of this kernel that the current device can hold (16, else
+// the portable 8), and the kernel's shared memory allowance; looked up once per device.
+cudaError_t max_cluster(int *ctas) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  *ctas = known[dev].load(std::memory_order_relaxed);
+  if (*ctas) return cudaSuccess;
+  e = cudaFuncSetAttribute(step_metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepMetaMaxSeqs * 12);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(step_metadata_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMetaMaxCtas);
+  cfg.blockDim = dim3(kMetaThreads);
+  cfg.dynamicSmemBytes = kStepMetaMaxSeqs * 12;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kMetaMaxCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, step_metadata_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // no answer: the portable size
+    clusters = 0;
+  }
+  *ctas = clusters > 0 ? kMetaMaxCtas : 8;
+  known[dev].store(*ctas, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+}  // namespace
+
 cudaError_t launch_step_metadata(const StepMetaArgs &a, unsigned int *err, cudaStream_t st) {
   const size_t smem = static_cast<size_t>(a.num_seqs) * 12;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(step_metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kStepMetaMaxSeqs * 12);
-    if (e != cudaSuccess) return e;
-  }
   // A CTA for every 2048 entries of the longer list (65536 tokens of 2048
-  // sequences: 71 us with one CTA, 11.9 with eight); up to 256 entries, 256
-  // threads start and meet sooner than 1024 (64 sequences' tokens: 5.0 us, 4.6).
+  // sequences: 71 us with one CTA, 12.0 with eight, 9.1 with sixteen); up to 256
+  // entries, 256 threads start and meet sooner than 1024 (4.6 us for 64 sequences, 5.0).
   const int64_t entries = a.max_tokens > a.num_seqs ? a.max_tokens : a.num_seqs;
+  int most = 0;
+  const cudaError_t e = max_cluster(&most);
+  if (e != cudaSuccess) return e;
   unsigned ctas = 1;
-  while (ctas * int64_t{2048} < entries && ctas < kMetaMaxCtas) ctas *= 2;
+  while (ctas * int64_t{2048} < entries && ctas < static_cast<unsigned>(most)) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(entries <= 256 ? 256 : kMetaThreads);
