@@ -159,7 +159,7 @@ def _p(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-_raw = None  # (current device's index, device index -> handle of its current stream)
+_raw = None  # (torch, current device's index, device index -> handle of its current stream)
 
 
 def _raw_getters():
@@ -168,7 +168,7 @@ def _raw_getters():
     global _raw
     if _raw is None:
         import torch
-        _raw = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+        _raw = (torch, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
                 getattr(torch._C, "_cuda_getCurrentRawStream",
                         lambda dev: torch.cuda.current_stream(dev).cuda_stream))
     return _raw
@@ -179,7 +179,7 @@ def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     import torch
-    return _raw_getters()[1](torch.cuda.current_device())
+    return _raw_getters()[2](torch.cuda.current_device())
 
 
 def photon_kv_cache_write(k, v, positions, slot_mapping, k_cache, v_cache, rope_theta,
@@ -333,78 +333,78 @@ def photon_kv_cache_fp4_record_bytes(head_dim: int) -> int:
 def _arg(what, t, dtype, shape, dev):
     """Address of t, which must be a contiguous tensor of this dtype (and
     shape) on the current device."""
+    if t.dtype is dtype and (shape is None or t.shape == shape) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device ({dev}), got {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to the library must be contiguous")
-    return t.data_ptr()
+    raise ValueError("tensors passed to the library must be contiguous")
 
 
 def _place(what, t, stream):
-    """(device, stream handle) of a call on the current device, which t must be on."""
-    device, raw_stream = _raw_getters()
+    """(torch, device, stream handle) of a call on the current device, which t must be on."""
+    torch, device, raw_stream = _raw or _raw_getters()
     dev = t.get_device()
     if dev < 0 or dev != device():
         raise ValueError(f"{what} must be on the current CUDA device, got {t.device}")
-    return dev, raw_stream(dev) if stream is None else stream.cuda_stream
+    return torch, dev, raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _rows(what, t):
-    """Shape and dtype code of rows [N, heads, head_dim]."""
-    if t.dim() != 3:
-        raise ValueError(f"{what} must have 3 dimensions, got {tuple(t.shape)}")
-    return t.shape, _dt(t)
+    """Shape of rows [N, heads, head_dim]."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have 3 dimensions, got {tuple(shape)}")
+    return shape
 
 
-def _pool(kv_cache, H, d, dev):
-    import torch
+def _pool(kv_cache, H, d, dev, dtype):
     shape = kv_cache.shape
     if len(shape) != 3 or shape[1] != H or shape[2] != 17 * d:
         raise ValueError(f"kv_cache must be [num_blocks, {H}, {17 * d}], got {tuple(shape)}")
-    return _arg("kv_cache", kv_cache, torch.uint8, None, dev), shape[0]
+    return _arg("kv_cache", kv_cache, dtype, None, dev), shape[0]
 
 
 def photon_kv_cache_write_fp4(k, v, positions, slot_mapping, kv_cache, rope_theta, rope_style="neox",
                               stream=None):
     """4-bit write: k, v [T, H_kv, d] (float32 or bfloat16); positions int32
     [T]; slot_mapping int64 [T]; kv_cache uint8 [num_blocks, H_kv, 17 * d]."""
-    import torch
-    (T, H, d), dt = _rows("k", k)
-    dev, st = _place("k", k, stream)
-    pool, nb = _pool(kv_cache, H, d, dev)
+    shape, dtype = _rows("k", k), k.dtype
+    T, H, d = shape
+    torch, dev, st = _place("k", k, stream)
+    pool, nb = _pool(kv_cache, H, d, dev, torch.uint8)
     style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
     _check(lib().photon_kv_cache_write_fp4(
-        _arg("k", k, k.dtype, None, dev), _arg("v", v, k.dtype, k.shape, dev),
+        _arg("k", k, dtype, None, dev), _arg("v", v, dtype, shape, dev),
         _arg("positions", positions, torch.int32, (T,), dev),
-        _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), pool, T, H, d, 16, nb, dt, float(rope_theta),
+        _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), pool, T, H, d, 16, nb, _dt(k), float(rope_theta),
         style, st), "photon_kv_cache_write_fp4")
 
 
 def photon_kv_cache_read_fp4(kv_cache, slot_mapping, k, v, stream=None):
     """Dequantised rows of the tokens at slot_mapping (int64 [T]) into k and v
     [T, H_kv, d] (float32 or bfloat16)."""
-    import torch
-    (T, H, d), dt = _rows("k", k)
-    dev, st = _place("k", k, stream)
-    pool, nb = _pool(kv_cache, H, d, dev)
+    shape, dtype = _rows("k", k), k.dtype
+    T, H, d = shape
+    torch, dev, st = _place("k", k, stream)
+    pool, nb = _pool(kv_cache, H, d, dev, torch.uint8)
     _check(lib().photon_kv_cache_read_fp4(
-        pool, _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), _arg("k", k, k.dtype, None, dev),
-        _arg("v", v, k.dtype, k.shape, dev), T, H, d, 16, nb, dt, st), "photon_kv_cache_read_fp4")
+        pool, _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), _arg("k", k, dtype, None, dev),
+        _arg("v", v, dtype, shape, dev), T, H, d, 16, nb, _dt(k), st), "photon_kv_cache_read_fp4")
 
 
 def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
                                       partition_size=512, workspace=None, stream=None):
     """Decode attention over a 4-bit pool (see photon_kv_cache_write_fp4); q
     bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
-    import torch
-    (B, Hq, d), _ = _rows("q", q)
-    dev, st = _place("q", q, stream)
+    shape = _rows("q", q)
+    B, Hq, d = shape
+    torch, dev, st = _place("q", q, stream)
     Hkv, W = kv_cache.shape[1], block_tables.shape[1]
-    pool, nb = _pool(kv_cache, Hkv, d, dev)
+    pool, nb = _pool(kv_cache, Hkv, d, dev, torch.uint8)
     if workspace is None:
         ws, ws_bytes = None, 0
     else:
@@ -412,7 +412,7 @@ def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, s
         ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib().photon_paged_attention_decode_fp4(
         _arg("q", q, torch.bfloat16, None, dev), pool, _arg("block_tables", block_tables, torch.int32, (B, W), dev),
-        _arg("context_lens", context_lens, torch.int32, (B,), dev), float(scale), _arg("out", out, out.dtype, q.shape, dev),
+        _arg("context_lens", context_lens, torch.int32, (B,), dev), float(scale), _arg("out", out, out.dtype, shape, dev),
         B, Hq, Hkv, d, 16, nb, W, int(max_context_len), int(partition_size), _dt(out), ws, ws_bytes, st),
         "photon_paged_attention_decode_fp4")
 
@@ -427,12 +427,11 @@ def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block
     token_seq, positions (int32) and slot_mapping (int64), all [max_tokens],
     context_lens int32 [B] and totals int32 [4] (tokens, longest context, free
     blocks, status)."""
-    import torch
     B, W = block_tables.shape
     M, = token_seq.shape
     blocks, = free_blocks.shape
+    torch, dev, st = _place("block_tables", block_tables, stream)
     i32 = torch.int32
-    dev, st = _place("block_tables", block_tables, stream)
     free = _arg("num_free", num_free, i32, (1,), dev)
     _check(lib().photon_build_step_metadata_device(
         _arg("num_computed_tokens", num_computed_tokens, i32, (B,), dev),
