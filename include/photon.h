@@ -400,7 +400,7 @@ size_t photon_kv_cache_fp4_record_bytes(int32_t head_dim);
  * scale and reads back as NaN.
  *   k, v      device [num_tokens][num_kv_heads][head_dim], in_dtype (f32 or bf16), 16-B aligned
  *   kv_cache  device 4-bit pool, 16-B aligned
- * head_dim 64 or 128, num_kv_heads <= 4096, num_blocks < 2^31
+ * head_dim 64 or 128, num_kv_heads <= 1024, num_blocks < 2^31
  * (PHOTON_ERR_UNSUPPORTED otherwise; the same for the two calls below).  Other
  * arguments and errors as photon_kv_cache_write.
  */

@@ -5,23 +5,37 @@
 //
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(x_j - m),  x_j = scale log2(e) <q, k_j>
 //
-//  * Records come straight from global memory into registers: every lane's
-//    fragment chunk is one coalesced 16-byte load (K plane, V plane, scales),
-//    so there is no shared-memory stage, barrier or fragment shuffle.  A step
-//    covers PP pages.  K of the next step is loaded as soon as this step's
-//    score MMAs have read their registers, V after its output MMAs.
+//  * A record (K, V and scales of one block and KV head) is contiguous and in
+//    fragment order, so a page is one bulk copy into the warp's shared-memory
+//    ring and every fragment one conflict-free 16-byte load.  A step covers PP
+//    pages; the lanes that hold a step's block-table entries issue its copies,
+//    ST steps ahead of the arithmetic and across item boundaries.  (Loads
+//    straight into registers, one step ahead, left 8 to 16 warps per SM waiting
+//    on latency: 384 us where the ring took 224, 128 contexts of up to 32k.)
+//  * S = K Q^T with the 16 tokens of a page as the MMA's rows and the query
+//    heads as its 8 columns: four MMAs per page and 64 dims, half of what the
+//    transposed product needs for up to 8 heads.  O^T = V^T P^T takes P through
+//    one movmatrix per 8 tokens.
 //  * Codes convert to f16 exactly in hardware (cvt.rn.f16x2.e2m1x2).  The
 //    scales never touch a code: a token's K scale multiplies its scores (per
 //    64 dims), its V scale the probability that weights it.
 //  * q enters as f16 after an exact power-of-two scaling of its row to
-//    [1, 2), so any bf16 q keeps its 8 bits down to 2^-24 of the row's largest
+//    [1, 2), so any bf16 q keeps its 8 bits down to 2^-14 of the row's largest
 //    value; the factor goes into the score scale, the scale's sign into q.
-//  * P is kept relative to 2^(m + E - 13), E the largest exponent of a V scale
-//    so far: p_j times its V scale then lies below 2^14 whatever the values'
-//    magnitude, and rounds to f16 with relative error 2^-12 down to 2^-28 of
-//    the largest.  For an fp32 output the remainder of that rounding follows
-//    in a second MMA (SPLIT), for a bf16 output (half a step: 2^-9) it would
-//    be lost anyway.  Sums, maxima and accumulators are fp32.
+//  * Weights are kept relative to 2^(m + E - 8), m within 2^6 of the largest
+//    score so far and E the largest exponent of a V scale: a weight times its V
+//    scale then lies below 2^15 whatever the values' magnitude, and rounds to
+//    f16 with relative error 2^-12 down to 2^-22 of the largest, by at most
+//    2^-33 of it below.  For an fp32 output the remainder of that rounding
+//    follows in a second MMA (SPLIT); for a bf16 output (half a step: 2^-8) it
+//    would be lost anyway.  Sums, maxima and accumulators are fp32.
+//
+// What bounds it: DRAM on long steps (with the merge, 128 contexts of up to 32k
+// tokens, d 64: 6.4 TB/s of records, 64 of d 128: 6.6; a copy reads and writes
+// 6.8), the issue slots right behind it (116 warp instructions per 1088-byte
+// page, ALU pipe 65 %, tensor pipe 32 %); start-up, uneven ends and the merge on
+// steps of some 30 pages per warp (64 ragged sequences of d 128: 4.1 TB/s);
+// latency on single requests.
 #include <atomic>
 #include <cuda_fp16.h>
 
@@ -32,11 +46,11 @@
 namespace photon {
 namespace {
 
-// Least exponent of the V scales that P follows: p is then at most 2^103 and
+// Least exponent of the V scales that P follows: p is then at most 2^104 and
 // its sum over a context stays in fp32.
 constexpr int kFp4MinExp = -90;
 // Base-2 distance that a score may pass the reference maximum by before the
-// reference moves: a weight times its V scale stays below 2^14 either way.
+// reference moves: a weight times its V scale stays below 2^15 either way.
 constexpr float kFp4Slack = 6.f;
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -118,11 +132,6 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
   Walker prod, w;  // the producer, ST steps ahead, and the consumer
   walker_start<BAL>(prod, a, lane, err, blockIdx.x * NW + warp, total_warps);
   w = prod;
-  // metadata only so far; pages, q and the workspace wait for the preceding kernel
-  pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && a.seg_count)  // the merge's mode
-    a.seg_count[static_cast<int64_t>(a.num_seqs) * a.num_q_heads] = BAL ? 1 : 0;
-
   // this lane's K (V) scale of token 4 (g >> 1) + 2n + (g & 1): half g & 1 of word n
   const uint32_t half_sel = (g & 1) ? 0x3244u : 0x1044u;
 
@@ -138,6 +147,10 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
                : -1;
   };
   if (prod.valid) ahead = table_entry(lane);
+  // metadata only so far; pages, q and the workspace wait for the preceding kernel
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.seg_count)  // the merge's mode
+    a.seg_count[static_cast<int64_t>(a.num_seqs) * a.num_q_heads] = BAL ? 1 : 0;
 
   // Starts the copies of the producer's next step into ring slot `slot`: the
   // lanes of its pages in the window each copy their record.  False past the
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
           sv[i][hh][1] = sr.w;
         }
       }
-      const int page = w.page, tok0 = (w.pg0 + page) * kBlockSize;
+      const int tok0 = (w.pg0 + w.page) * kBlockSize;
       w.page += PP;
       if (valid) {  // no page of the step in the pool: nothing to add
         // tokens past the context, of absent pages: weight 0 (their bytes may hold anything)
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
           for (int j = 0; j < 2; ++j) {
             const float m_run = fmaxf(m_lim[j] - kFp4Slack, (j ? m1 : m0) * sl[j]);
             m_lim[j] = m_run + kFp4Slack;
-            const float ref = m_run + (static_cast<float>(e_run) - (13.f - kFp4Slack));
+            const float ref = m_run + (static_cast<float>(e_run) - (14.f - kFp4Slack));
             alpha[j] = exp2_approx(m_ref[j] - ref);
             m_ref[j] = ref;
             l_run[j] *= alpha[j];
@@ -478,6 +491,9 @@ cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t
   return launch_pdl(kern, dim3(grid), dim3(NW * 32), SMEM, stream, la, err);
 }
 
+// PP, ST, MIN_CTAS: CTAs of four warps; PP1, ST1, NW1: the one CTA per SM of
+// long steps.  Short steps take few pages at once (d 64: one request of 1024
+// tokens 6.8 us with four, 6.2 with two; 16 contexts of up to 2048 11.8, 11.1).
 template <int D, int PP, int ST, int MIN_CTAS, int PP1, int ST1, int NW1, bool SPLIT>
 cudaError_t launch_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
   if (!balanced_pieces(a)) return launch_fp4_kern<D, PP, ST, 4, MIN_CTAS, false, SPLIT>(a, err, stream, nullptr);

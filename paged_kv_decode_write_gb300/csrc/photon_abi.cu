@@ -568,7 +568,8 @@ int check_fp4_pool(int32_t num_kv_heads, int32_t head_dim, int32_t block_size, i
   if (head_dim != 64 && head_dim != 128) return PHOTON_ERR_UNSUPPORTED;
   if (num_blocks > INT64_MAX / (static_cast<int64_t>(num_kv_heads) * 17 * head_dim))
     return PHOTON_ERR_INVALID_ARG;
-  if (num_blocks > INT32_MAX || num_kv_heads > 4096) return PHOTON_ERR_UNSUPPORTED;  // 32-bit block ids, offsets in a block
+  // 32-bit block ids; a grid has a warp for every KV head
+  if (num_blocks > INT32_MAX || num_kv_heads > 1024) return PHOTON_ERR_UNSUPPORTED;
   return PHOTON_OK;
 }
 

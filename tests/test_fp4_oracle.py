@@ -162,7 +162,7 @@ def test_invalid_arguments_are_refused(call, bad):
 
 
 @pytest.mark.parametrize("call,bad", [
-    (_w, dict(d=32)), (_w, dict(d=256)), (_w, dict(d=96)), (_w, dict(bs=32)), (_w, dict(nb=2 ** 31)), (_w, dict(H=4097)), (_r, dict(nb=2 ** 31)), (_r, dict(d=256)), (_r, dict(bs=8)),
+    (_w, dict(d=32)), (_w, dict(d=256)), (_w, dict(d=96)), (_w, dict(bs=32)), (_w, dict(nb=2 ** 31)), (_w, dict(H=1025)), (_d, dict(Hkv=1025, Hq=1025)), (_r, dict(nb=2 ** 31)), (_r, dict(d=256)), (_r, dict(bs=8)),
     (_d, dict(d=32)), (_d, dict(d=256)), (_d, dict(Hq=6)), (_d, dict(Hq=32)), (_d, dict(bs=8)), (_d, dict(mc=2 ** 31 - 16, W=2 ** 27, part=2 ** 30, ws=256, wsb=2 ** 40)),
     (_m, dict(bs=32)), (_m, dict(B=16385)), (_m, dict(nb=2 ** 31)), (_m, dict(B=16384, W=2 ** 17)),
 ])

@@ -488,6 +488,31 @@ def test_decode_on_another_stream_and_two_at_once():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
+def test_many_kv_heads():
+    """As many KV heads as a call takes: write, read and decode."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(12)
+    H, d, ctx = 1024, 64, [40, 17]
+    pool = _random_pool(rng, 6, H, d)
+    bt = _tables(rng, ctx, 6)
+    q, qt = _storage(rng.standard_normal((2, H, d)), "bf16")
+    for part in (16, 512):
+        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.1, torch.float32, part).double().cpu().numpy()
+        ref = fp4.paged_attention(q, pool, bt, ctx, 0.1)
+        kd, vd = fp4.dequant(pool, d)
+        assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, 0.1, False, ref)).all()
+    k, kt = _storage(rng.standard_normal((2, H, d)), "bf16")
+    dev, slots = _dev(pool.copy()), np.array([5, 90], np.int64)
+    pk.photon_kv_cache_write_fp4(kt, kt, _dev(np.array([3, 4], np.int32)), _dev(slots), dev, 1e4)
+    fp4.write(k, k, [3, 4], slots, pool, 1e4)
+    assert np.array_equal(dev.cpu().numpy(), pool)
+    ko, vo = torch.empty_like(kt), torch.empty_like(kt)
+    pk.photon_kv_cache_read_fp4(dev, _dev(slots), ko, vo)
+    want = fp4.dequant(pool, d)[1][slots // 16, :, slots % 16]
+    assert torch.equal(vo.cpu(), torch.from_numpy(want).float().bfloat16())
+
+
 def test_decode_repeats_bit_for_bit():
     torch = _torch()
     pk = ensure_built()
