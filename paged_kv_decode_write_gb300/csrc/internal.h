@@ -177,6 +177,7 @@ cudaError_t launch_kv_cache_write_fp4(const WriteArgs &a, photon_dtype in_dt, un
 cudaError_t launch_kv_cache_read_fp4(const Fp4ReadArgs &a, photon_dtype out_dt, unsigned int *err,
                                      cudaStream_t st);
 cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st);
+cudaError_t launch_decode_merge_fp4(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_step_metadata(const StepMetaArgs &a, unsigned int *err, cudaStream_t st);
 
 // Every host-side check of photon_paged_attention_decode except the workspace

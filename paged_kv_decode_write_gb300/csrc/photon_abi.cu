@@ -661,7 +661,7 @@ int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = cuda_status(launch_decode_partial_fp4(p.args, err, st));
   if (rc != PHOTON_OK || p.ws.total == 0) return rc;
-  return cuda_status(launch_decode_reduce(p.args, st));
+  return cuda_status(launch_decode_merge_fp4(p.args, st));
 }
 
 int photon_build_step_metadata_device(const int32_t *num_computed_tokens, const int32_t *num_new_tokens,
