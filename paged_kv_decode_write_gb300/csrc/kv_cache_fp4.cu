@@ -16,7 +16,6 @@
 #include <cmath>
 
 #include "fp4.cuh"
-#include "rope.cuh"
 
 namespace photon {
 namespace {
@@ -42,7 +41,7 @@ struct TurnTable {
 
 constexpr double kTurn = 6.283185307179586476925286766559;
 
-// Taylor series on |x| <= pi / 4 (17 terms are far past fp64's precision).
+// Taylor series on |x| <= pi / 4 (12 terms are past fp64's precision).
 constexpr double taylor_sin(double x) {
   double term = x, sum = x;
   for (int n = 1; n < 12; ++n) {
@@ -188,10 +187,11 @@ __device__ __forceinline__ float rcp_approx(float s) {
 }
 
 // x / s close enough for the code: y0 = x is, is the reciprocal within an ulp,
-// corrected once by its exact residual is the quotient when that has few bits, a midpoint of two codes among
-// them, and within an ulp otherwise.  A bf16 x (8 bits) over a bf16 s is never
-// within 2^-11 of a midpoint without being it; an fp32 x may be, and its y may
-// round onto the midpoint: the residual's sign then says which side it is on.
+// corrected once by its exact residual is the quotient when that has few bits,
+// a midpoint of two codes among them, and within an ulp otherwise.  A bf16 x
+// (8 bits) over a bf16 s is never within 2^-11 of a midpoint without being it;
+// an fp32 x may be, and its y may round onto the midpoint: the residual's sign
+// then says which side it is on.
 template <typename Tag>
 __device__ __forceinline__ float quotient(float x, float s, float is) {
   const float y0 = x * is;
