@@ -135,9 +135,24 @@ __device__ __forceinline__ float rotated(float u, float w, float ch, float cl, f
   return s + (se + (fmaf(u, cl, pe) + fmaf(w, tl, qe)));
 }
 
-__device__ __forceinline__ float stored(float v, float) { return v; }
-__device__ __forceinline__ float stored(float v, __nv_bfloat16) {
-  return __bfloat162float(__float2bfloat16_rn(v));
+// The same of bf16 u and w, rounded to bf16 as well; ch and th have 16 bits
+// (table_entry), so that both products are exact and need no remainder.
+__device__ __forceinline__ float rotated_bf16(float u, float w, float ch, float cl, float th, float tl) {
+  float s, se;
+  two_sum(__fmul_rn(u, ch), __fmul_rn(w, th), s, se);
+  return __bfloat162float(__float2bfloat16_rn(s + (se + fmaf(u, cl, w * tl))));
+}
+
+// A position's (cos, sin) as the rotation of T takes it.
+template <typename T>
+__device__ __forceinline__ float4 table_entry(unsigned long long turn) {
+  float4 p = cos_sin_turn(turn);
+  if (sizeof(T) == 2) {
+    const float c = __uint_as_float(__float_as_uint(p.x) & 0xffffff00u);
+    const float s = __uint_as_float(__float_as_uint(p.z) & 0xffffff00u);
+    p = make_float4(c, (p.x - c) + p.y, s, (p.z - s) + p.w);
+  }
+  return p;
 }
 
 // The 8 pairs of a lane, rotated and rounded to fp32 and then to the storage
@@ -153,8 +168,13 @@ __device__ __forceinline__ void rotate_lane(float (&x0)[8], float (&x1)[8], cons
     float &w = GPTJ ? (i < 4 ? x0[2 * i + 1] : x1[2 * i - 7]) : x1[i];
     const float4 p = cs[i * stride];
     const float a = u, b = w;
-    u = stored(rotated(a, b, p.x, p.y, -p.z, -p.w), T{});
-    w = stored(rotated(b, a, p.x, p.y, p.z, p.w), T{});
+    if constexpr (sizeof(T) == 2) {
+      u = rotated_bf16(a, b, p.x, p.y, -p.z, -p.w);
+      w = rotated_bf16(b, a, p.x, p.y, p.z, p.w);
+    } else {
+      u = rotated(a, b, p.x, p.y, -p.z, -p.w);
+      w = rotated(b, a, p.x, p.y, p.z, p.w);
+    }
   }
 }
 
@@ -294,7 +314,7 @@ __global__ void __launch_bounds__(kFp4Threads, 4)
       const int tt = i / HALF, pair = i % HALF;
       // NEOX: lane w takes pairs 8w ..; GPT-J: 4w .. of either half
       const int at = gptj ? (pair / (D / 4) * 4 + pair % 4) * LPR + pair % (D / 4) / 4 : pair % 8 * LPR + pair / 8;
-      cs[tt][at] = cos_sin_turn(
+      cs[tt][at] = table_entry<T>(
           static_cast<unsigned long long>(static_cast<long long>(a.positions[t0 + tt])) * a.turns[pair]);
     }
   __syncthreads();
