@@ -107,7 +107,9 @@ struct Fp4Ring {
   static_assert(ST * PP <= 32, "a bit per page of the ring");
 };
 
-template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT>
+// TEAM: an item belongs to a CTA, whose warps take a share of its pages each
+// and meet in shared memory at its end (else every warp has items of its own).
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, bool TEAM>
 __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     paged_decode_fp4_kernel(const DecodeArgs a, unsigned int *err) {
   using R = Fp4Ring<D, PP, ST, NW>;
@@ -127,10 +129,24 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
   if constexpr (BAL) prefetch_tables_l2(a);
   pdl_launch_dependents();
   const uint64_t policy = l2_evict_first_policy();
-  const int total_warps = gridDim.x * NW;
+  const int workers = gridDim.x * (TEAM ? 1 : NW);  // that take items
 
+  // this warp's share of an item's pages: whole steps, in order
+  auto share = [&](Walker &w) {
+    if constexpr (TEAM) {
+      const int part = ((w.n_pages + NW - 1) / NW + PP - 1) / PP * PP;
+      const int lo = min(warp * part, w.n_pages);
+      w.n_pages = min(part, w.n_pages - lo);
+      w.pg0 += lo;
+    }
+  };
+  auto next_item = [&](Walker &w) {
+    walker_next<BAL>(w, a, lane, err, workers);
+    if (w.valid) share(w);
+  };
   Walker prod, w;  // the producer, ST steps ahead, and the consumer
-  walker_start<BAL>(prod, a, lane, err, blockIdx.x * NW + warp, total_warps);
+  walker_start<BAL>(prod, a, lane, err, TEAM ? static_cast<int>(blockIdx.x) : blockIdx.x * NW + warp, total_warps);
+  if (prod.valid) share(prod);
   w = prod;
   // this lane's K (V) scale of token 4 (g >> 1) + 2n + (g & 1): half g & 1 of word n
   const uint32_t half_sel = (g & 1) ? 0x3244u : 0x1044u;
@@ -157,7 +173,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
   // warp's last step.
   auto issue_next = [&](int slot) -> bool {
     while (prod.valid && prod.page >= prod.n_pages) {
-      walker_next<BAL>(prod, a, lane, err, total_warps);
+      next_item(prod);
       if (prod.valid) ahead = table_entry(lane);
     }
     if (!prod.valid) return false;
@@ -187,6 +203,9 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
   for (int k = 0; k < ST; ++k)
     if (!issue_next(k)) break;
 
+  bool gave_up = false;
+  __shared__ float team_o[TEAM ? NW - 1 : 1][HH * 16][32];  // of warps 1 ..: accumulators,
+  __shared__ float team_ml[TEAM ? NW - 1 : 1][4][32];       // references and sums
   while (w.valid) {
     // ---- a new item: the query group
     uint32_t qb[HH][4][2];     // q of head g, dims 16c + 4kt + {0,1}, {2,3} of each plane
@@ -244,12 +263,14 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     int e_run = kFp4MinExp;
     uint32_t e_lim = 0;
 
-    while (w.page < w.n_pages) {
+    while (w.page < w.n_pages && !gave_up) {
       const bool landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[c_slot], c_phase, kWaitBudgetCycles));
       if (!landed) {
         if (lane == 0) atomicOr(err, PHOTON_DEVERR_WAIT_TIMEOUT);
         drain_async_copies();
-        return;
+        if constexpr (!TEAM) return;
+        gave_up = true;  // the team's other warps still wait for this one
+        break;
       }
       const uint32_t valid = (valid_bits >> (PP * c_slot)) & ((1u << PP) - 1);
       const unsigned char *stage = stages + c_slot * R::STAGE;
@@ -401,12 +422,59 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
       }
     }
 
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], d);
+    if constexpr (TEAM) {  // warp 0 adds the others' shares, in order
+      if (warp > 0) {
+#pragma unroll
+        for (int i = 0; i < HH * 16; ++i) team_o[warp - 1][i][lane] = o[i / 16][i / 4 % 4][i % 4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          team_ml[warp - 1][j][lane] = m_ref[j];
+          team_ml[warp - 1][2 + j][lane] = l_run[j];
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {
+        float M[2] = {m_ref[0], m_ref[1]}, f[NW][2];
+#pragma unroll
+        for (int k = 0; k < NW - 1; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) M[j] = fmaxf(M[j], team_ml[k][j][lane]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f[0][j] = m_ref[j] == -INFINITY ? 0.f : exp2_approx(m_ref[j] - M[j]);
+          l_run[j] *= f[0][j];
+          m_ref[j] = M[j];
+        }
+#pragma unroll
+        for (int k = 0; k < NW - 1; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float mk = team_ml[k][j][lane];
+            f[k + 1][j] = mk == -INFINITY ? 0.f : exp2_approx(mk - M[j]);
+            l_run[j] = fmaf(team_ml[k][2 + j][lane], f[k + 1][j], l_run[j]);
+          }
+#pragma unroll
+        for (int i = 0; i < HH * 16; ++i) {
+          float &x = o[i / 16][i / 4 % 4][i % 4];
+          x *= f[0][i & 1];
+#pragma unroll
+          for (int k = 0; k < NW - 1; ++k) x = fmaf(team_o[k][i][lane], f[k + 1][i & 1], x);
+        }
+      }
+      __syncthreads();  // read before the next item's shares are written
+      if (warp > 0) {
+        next_item(w);
+        continue;
+      }
+    }
     // ---- item done: o[hh][mt][2r + j] is head 2c + j, dim 64 hh + 8g + 2mt + r
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float l = l_run[j];
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      const float l = l_run[j];
       const int head = 2 * c + j;
       if (head >= G) continue;
       const int64_t qrow = static_cast<int64_t>(w.s) * a.num_q_heads + w.h * G + head;
@@ -438,7 +506,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
         a.l_part[prow] = l;
       }
     }
-    walker_next<BAL>(w, a, lane, err, total_warps);
+    next_item(w);
   }
 }
 
@@ -459,10 +527,28 @@ inline int64_t page_bound(const DecodeArgs &a) {
          a.num_kv_heads;
 }
 
-template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT>
-cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *full) {
+// When items are few and long, a CTA of four warps takes each: the piece count
+// of a row is bounded by the partition size (the workspace has no more slots),
+// and an item of 32 pages keeps a single warp busy for 10 us however idle the
+// GPU.  One warp per item -> a team: 30 sequences of 518 tokens, two KV heads,
+// partitions of 512: 15.0 -> 9.6 us; 9 of 1432, four heads of d 128, fp32 out,
+// 512: 25.2 -> 12.5; 75 of 500, eight heads, 512: 16.5 -> 9.9; 64 of 128, 128:
+// 6.9 -> 5.8; 16 of 1024, 128: 8.4 -> 8.2.  Chosen when all items fit the GPU
+// as CTAs at once and an item may have kFp4TeamPages pages or more.
+constexpr int kFp4TeamPages = 8;
+
+inline bool few_long_items(const DecodeArgs &a, int64_t items, int64_t ctas) {
+  const int longest = a.partition_size < a.ctx_cap ? a.partition_size : a.ctx_cap;
+  return items <= ctas && longest >= kFp4TeamPages * kBlockSize;
+}
+
+enum class Fp4Fit { kAlways, kLongSteps, kTeams };  // when launch_fp4_kern takes a step
+
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, Fp4Fit FIT>
+cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
+  constexpr bool TEAM = FIT == Fp4Fit::kTeams;
   constexpr int SMEM = Fp4Ring<D, PP, ST, NW>::SMEM;
-  auto kern = paged_decode_fp4_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT>;
+  auto kern = paged_decode_fp4_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, TEAM>;
   static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -478,29 +564,38 @@ cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t
     occupancy[dev].store(occ, std::memory_order_relaxed);
   }
   const int64_t items = static_cast<int64_t>(a.num_seqs) * a.max_partitions * a.num_kv_heads;
-  const int64_t warps_cap = static_cast<int64_t>(device_sm_count()) * occ * NW;
-  if (full) {  // only for a full grid of long runs
-    *full = items >= warps_cap && page_bound(a) >= kFp4MinPagesPerWarp * warps_cap;
-    if (!*full) return cudaSuccess;
-  }
+  const int64_t ctas_cap = static_cast<int64_t>(device_sm_count()) * occ;
+  const int64_t warps_cap = ctas_cap * NW;
+  *taken = FIT == Fp4Fit::kAlways ||
+           (FIT == Fp4Fit::kTeams && few_long_items(a, items, ctas_cap)) ||
+           (FIT == Fp4Fit::kLongSteps && items >= warps_cap && page_bound(a) >= kFp4MinPagesPerWarp * warps_cap);
+  if (!*taken || items == 0) return cudaSuccess;
   const int64_t warps = items < warps_cap ? items : warps_cap;
-  const int grid = static_cast<int>((warps + NW - 1) / NW);
-  if (grid == 0) return cudaSuccess;
+  const int64_t grid = TEAM ? items : (warps + NW - 1) / NW;
   DecodeArgs la = a;
   la.balanced = BAL ? 1 : 0;
-  return launch_pdl(kern, dim3(grid), dim3(NW * 32), SMEM, stream, la, err);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(NW * 32), SMEM, stream, la, err);
 }
 
 // PP, ST, MIN_CTAS: CTAs of four warps; PP1, ST1, NW1: the one CTA per SM of
 // long steps.  Short steps take few pages at once (d 64: one request of 1024
 // tokens 6.8 us with four, 6.2 with two; 16 contexts of up to 2048 11.8, 11.1).
+template <int D, int PP, int ST, int MIN_CTAS, int PP1, int ST1, int NW1, bool SPLIT, bool BAL>
+cudaError_t launch_fp4_split(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
+  bool taken = false;
+  cudaError_t e = launch_fp4_kern<D, PP, ST, 4, 1, BAL, SPLIT, Fp4Fit::kTeams>(a, err, stream, &taken);
+  if (e != cudaSuccess || taken) return e;
+  if constexpr (BAL) {
+    e = launch_fp4_kern<D, PP1, ST1, NW1, 1, true, SPLIT, Fp4Fit::kLongSteps>(a, err, stream, &taken);
+    if (e != cudaSuccess || taken) return e;
+  }
+  return launch_fp4_kern<D, PP, ST, 4, MIN_CTAS, BAL, SPLIT, Fp4Fit::kAlways>(a, err, stream, &taken);
+}
+
 template <int D, int PP, int ST, int MIN_CTAS, int PP1, int ST1, int NW1, bool SPLIT>
 cudaError_t launch_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
-  if (!balanced_pieces(a)) return launch_fp4_kern<D, PP, ST, 4, MIN_CTAS, false, SPLIT>(a, err, stream, nullptr);
-  bool full = false;
-  const cudaError_t e = launch_fp4_kern<D, PP1, ST1, NW1, 1, true, SPLIT>(a, err, stream, &full);
-  if (e != cudaSuccess || full) return e;
-  return launch_fp4_kern<D, PP, ST, 4, MIN_CTAS, true, SPLIT>(a, err, stream, nullptr);
+  return balanced_pieces(a) ? launch_fp4_split<D, PP, ST, MIN_CTAS, PP1, ST1, NW1, SPLIT, true>(a, err, stream)
+                            : launch_fp4_split<D, PP, ST, MIN_CTAS, PP1, ST1, NW1, SPLIT, false>(a, err, stream);
 }
 
 // Merge of a row's pieces: out = sum_p o_p 2^(m_p - M) / sum_p l_p 2^(m_p - M).

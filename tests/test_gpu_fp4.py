@@ -513,6 +513,57 @@ def test_many_kv_heads():
     assert torch.equal(vo.cpu(), torch.from_numpy(want).float().bfloat16())
 
 
+@pytest.mark.parametrize("ctx,part", [
+    ([500, 1, 0, 128, 129, 33, 16, 512], 512),                                   # one piece per row, no workspace
+    ([0, 0, 1, 15, 16, 17, 32, 0, 130, 1000, 47, 0, 1, 1, 1, 1, 1, 64, 5, 0], 128),  # runs over many sequences
+    ([16 * k + k % 3 for k in range(1, 36)], 256),                               # every share of 1 to 16 pages
+    ([3001], 512), ([700, 4090], 1024)])
+@pytest.mark.parametrize("H,G,d", [(2, 4, 64), (1, 8, 128), (3, 1, 128), (4, 2, 64)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_decode_of_few_long_pieces(ctx, part, H, G, d, out):
+    """Batches far smaller than the GPU with large partitions: the warps of a
+    CTA share each piece.  Missing blocks empty some of the shares; every call
+    gives the same bits."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(len(ctx) + part + d)
+    nb = sum(-(-c // 16) for c in ctx) + 1
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    dev = _dev(pool)
+    pk.photon_device_errors()
+    a = _decode(pk, qt, dev, bt, ctx, d ** -0.5, dt, part, extra_rows=1)
+    assert torch.equal(a, _decode(pk, qt, dev, bt, ctx, d ** -0.5, dt, part, extra_rows=1))
+    assert (a[len(ctx):] == -7.0).all()
+    ref = fp4.paged_attention(q, pool, bt, ctx, d ** -0.5)
+    kd, vd = fp4.dequant(pool, d)
+    q64 = oracle.to_f64(q)
+    tol = _tolerance(q64, kd, vd, ctx, d ** -0.5, out == "bf16", ref)
+    assert (np.abs(a[:len(ctx)].double().cpu().numpy() - ref) <= tol).all()
+    assert pk.photon_device_errors() == 0
+    # a sequence's first pages alone, then its last one alone, are left
+    s = int(np.argmax(ctx))
+    n = -(-ctx[s] // 16)
+    for keep in (range(0, 2), range(n - 1, n)):
+        some = bt.copy()
+        some[s, [i for i in range(n) if i not in keep]] = -1
+        got = _decode(pk, qt, dev, some, ctx, d ** -0.5, dt, part)
+        assert pk.photon_device_errors() == pk.DEVERR_BLOCK_RANGE
+        rest = [i for i in range(len(ctx)) if i != s]
+        assert torch.equal(got[rest], a[rest])
+        tokens = [p for p in range(ctx[s]) if p // 16 in keep]
+        for h in range(H * G):
+            ks = np.array([kd[bt[s, p // 16], h // G, p % 16] for p in tokens])
+            vs = np.array([vd[bt[s, p // 16], h // G, p % 16] for p in tokens])
+            x = ks @ q64[s, h] * d ** -0.5
+            w = np.exp(x - x.max())
+            want = w @ vs / w.sum()
+            lim = _tolerance(q64, kd, vd, ctx, d ** -0.5, out == "bf16", want)
+            assert (np.abs(got[s, h].double().cpu().numpy() - want) <= lim).all()
+
+
 def test_decode_repeats_bit_for_bit():
     torch = _torch()
     pk = ensure_built()
