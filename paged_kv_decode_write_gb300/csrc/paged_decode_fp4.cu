@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     if (w.valid) share(w);
   };
   Walker prod, w;  // the producer, ST steps ahead, and the consumer
-  walker_start<BAL>(prod, a, lane, err, TEAM ? static_cast<int>(blockIdx.x) : blockIdx.x * NW + warp, total_warps);
+  walker_start<BAL>(prod, a, lane, err, TEAM ? blockIdx.x : blockIdx.x * NW + warp, workers);
   if (prod.valid) share(prod);
   w = prod;
   // this lane's K (V) scale of token 4 (g >> 1) + 2n + (g & 1): half g & 1 of word n
