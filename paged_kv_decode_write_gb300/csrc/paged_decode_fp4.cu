@@ -36,6 +36,7 @@
 // page, ALU pipe 65 %, tensor pipe 32 %); start-up, uneven ends and the merge on
 // steps of some 30 pages per warp (64 ragged sequences of d 128: 4.1 TB/s);
 // latency on single requests.
+#include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
 
@@ -530,16 +531,25 @@ inline int64_t page_bound(const DecodeArgs &a) {
 // When items are few and long, a CTA of four warps takes each: the piece count
 // of a row is bounded by the partition size (the workspace has no more slots),
 // and an item of 32 pages keeps a single warp busy for 10 us however idle the
-// GPU.  One warp per item -> a team: 30 sequences of 518 tokens, two KV heads,
-// partitions of 512: 15.0 -> 9.6 us; 9 of 1432, four heads of d 128, fp32 out,
-// 512: 25.2 -> 12.5; 75 of 500, eight heads, 512: 16.5 -> 9.9; 64 of 128, 128:
-// 6.9 -> 5.8; 16 of 1024, 128: 8.4 -> 8.2.  Chosen when all items fit the GPU
-// as CTAs at once and an item may have kFp4TeamPages pages or more.
-constexpr int kFp4TeamPages = 8;
+// GPU.  Teams are used where the least piece, or an item without a workspace,
+// has
+//  * 8 pages, without a workspace 4, and all items fit the GPU as CTAs at once:
+//    one warp per item -> a team, 64 sequences of 128 tokens 6.9 -> 5.8 us, 8 of
+//    1024 in pieces of 8 pages 7.1 -> 6.6 (of 4 pages: 4 of 1024 5.7 -> 5.9),
+//    30 of 518 (two KV heads, 32 pages) 15.0 -> 9.6, one of 32768 17.9 -> 10.0,
+//    9 of 1432 (d 128, fp32 output) 25.2 -> 12.5;
+//  * 16 pages, with more items: pieces as long as the workspace allows must
+//    leave warps idle (60 ragged sequences of up to 1000 tokens, d 128, 28.2 ->
+//    19.3; 40 of up to 1024, 14.4 -> 12.0), items be at most two to a CTA (64 of
+//    500, d 128, 21.3 -> 15.8).  With 8 pages 16 of 2048 10.2 -> 13.6.
+constexpr int kFp4TeamPages = 8, kFp4TeamItemPages = 4, kFp4TeamManyPages = 16;
 
-inline bool few_long_items(const DecodeArgs &a, int64_t items, int64_t ctas) {
-  const int longest = a.partition_size < a.ctx_cap ? a.partition_size : a.ctx_cap;
-  return items <= ctas && longest >= kFp4TeamPages * kBlockSize;
+template <bool BAL>
+inline bool team_step(const DecodeArgs &a, int64_t items, int64_t ctas, int warps_per_cta) {
+  const int longest = (a.partition_size < a.ctx_cap ? a.partition_size : a.ctx_cap) / kBlockSize;
+  if (items <= ctas) return longest >= (BAL ? kFp4TeamPages : kFp4TeamItemPages);
+  if (longest < kFp4TeamManyPages || a.num_kv_heads > ctas / 4) return false;
+  return BAL ? page_bound(a) <= ctas * warps_per_cta * (a.partition_size / kBlockSize) : items <= 2 * ctas;
 }
 
 enum class Fp4Fit { kAlways, kLongSteps, kTeams };  // when launch_fp4_kern takes a step
@@ -567,11 +577,11 @@ cudaError_t launch_fp4_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t
   const int64_t ctas_cap = static_cast<int64_t>(device_sm_count()) * occ;
   const int64_t warps_cap = ctas_cap * NW;
   *taken = FIT == Fp4Fit::kAlways ||
-           (FIT == Fp4Fit::kTeams && few_long_items(a, items, ctas_cap)) ||
+           (FIT == Fp4Fit::kTeams && team_step<BAL>(a, items, ctas_cap, NW)) ||
            (FIT == Fp4Fit::kLongSteps && items >= warps_cap && page_bound(a) >= kFp4MinPagesPerWarp * warps_cap);
   if (!*taken || items == 0) return cudaSuccess;
-  const int64_t warps = items < warps_cap ? items : warps_cap;
-  const int64_t grid = TEAM ? items : (warps + NW - 1) / NW;
+  const int64_t workers = std::min(items, TEAM ? ctas_cap : warps_cap);
+  const int64_t grid = TEAM ? workers : (workers + NW - 1) / NW;
   DecodeArgs la = a;
   la.balanced = BAL ? 1 : 0;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(NW * 32), SMEM, stream, la, err);

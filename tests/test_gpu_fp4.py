@@ -517,7 +517,9 @@ def test_many_kv_heads():
     ([500, 1, 0, 128, 129, 33, 16, 512], 512),                                   # one piece per row, no workspace
     ([0, 0, 1, 15, 16, 17, 32, 0, 130, 1000, 47, 0, 1, 1, 1, 1, 1, 64, 5, 0], 128),  # runs over many sequences
     ([16 * k + k % 3 for k in range(1, 36)], 256),                               # every share of 1 to 16 pages
-    ([3001], 512), ([700, 4090], 1024)])
+    ([3001], 512), ([700, 4090], 1024),
+    ([500 - 3 * k for k in range(160)], 512),                                    # two items to some CTAs
+    ([(97 * k) % 1200 for k in range(90)], 256)])                                # runs over pieces of 16 pages, many
 @pytest.mark.parametrize("H,G,d", [(2, 4, 64), (1, 8, 128), (3, 1, 128), (4, 2, 64)])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_decode_of_few_long_pieces(ctx, part, H, G, d, out):
