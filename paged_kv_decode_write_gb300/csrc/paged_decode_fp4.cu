@@ -110,6 +110,8 @@ struct Fp4Ring {
 
 // TEAM: an item belongs to a CTA, whose warps take a share of its pages each
 // and meet in shared memory at its end (else every warp has items of its own).
+// They walk the same items, so their barriers match; a warp that gave up on a
+// copy still walks on to them.
 template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, bool TEAM>
 __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     paged_decode_fp4_kernel(const DecodeArgs a, unsigned int *err) {
