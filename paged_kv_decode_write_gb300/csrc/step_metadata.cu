@@ -200,10 +200,13 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
       from = __shfl_sync(0xffffffffu, s[i], 31);
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) nc[i] = a.num_computed[s[i]];
+    for (int i = 0; i < N; ++i) nc[i] = i < turns ? a.num_computed[s[i]] : 0;
     int32_t id[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      id[i] = -1;
+      p[i] = 0;
+      if (i >= turns) continue;  // s[i] need not own x[i]: its row may not reach that far, nor the stack
       p[i] = nc[i] + (x[i] - tok[s[i]]);
       const int have = (nc[i] + kBlockSize - 1) / kBlockSize, b = p[i] / kBlockSize;
       id[i] = __ldcg(b < have ? a.block_tables + static_cast<int64_t>(s[i]) * a.max_blocks_per_seq + b

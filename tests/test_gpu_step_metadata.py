@@ -298,3 +298,32 @@ def test_prefix_read_back_feeds_the_bf16_prefill():
                                          0.125)
     assert np.abs(out.cpu().numpy() - ref).max() <= 5e-3
     assert pk.photon_device_errors() == 0
+
+
+@pytest.mark.parametrize("B", [1, 32, 33, 64, 65, 128, 200, 255, 256, 257, 1025])
+@pytest.mark.parametrize("grown", [0, 3])
+def test_a_step_that_takes_the_last_blocks(B, grown):
+    """A step that leaves no block free, and one that needs none of an empty
+    stack: the stack lies between other data, which stays as it was, and no
+    value of which reaches a result."""
+    torch = _torch()
+    pk = ensure_built()
+    grown = min(grown, B)
+    nb = 2 * B + grown
+    perm = np.random.default_rng(B).permutation(nb).astype(np.int32)
+    nc = np.full(B, 20, np.int32)
+    nc[:grown] = 32
+    nn = np.ones(B, np.int32)
+    tables = np.concatenate([perm[:2 * B].reshape(B, 2), np.full((B, 1), -1, np.int32)], 1)
+    stack = [int(x) for x in perm[2 * B:]]
+    dev = Dev(tables, stack, nb, B)
+    room = torch.full((nb + 256,), 2 ** 30, dtype=torch.int32, device="cuda")
+    room[128:128 + nb] = dev.free
+    dev.free = room[128:128 + nb]
+    pk.photon_device_errors()
+    dev.step(pk, nc, nn)
+    want = fp4.step_metadata(nc, nn, tables, stack, B, nb)
+    assert want[-1] == 0 and want[1] == []
+    dev.check(want)
+    assert (room[:128] == 2 ** 30).all() and (room[128 + nb:] == 2 ** 30).all()
+    assert pk.photon_device_errors() == 0
