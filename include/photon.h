@@ -432,7 +432,9 @@ int photon_kv_cache_read_fp4(const void *kv_cache, const int64_t *slot_mapping, 
  * (already rotated) of any magnitude.  The scores, softmax and sums are fp32;
  * a softmax weight times its V scale enters the second product in f16 (11
  * significant bits) for a bf16 output, as f16 and its f16 remainder (22) for
- * an fp32 one.  Workspace as for photon_paged_attention_decode; the split-K
+ * an fp32 one, scaled by the largest V scale of the same 64 dims.  K and V may
+ * have any magnitude whose sums fit fp32: |k| below 2^119, |v| summed over a
+ * context below 2^127, |scale| times a row's largest |q| below 2^127.  Workspace as for photon_paged_attention_decode; the split-K
  * pieces are equal runs of pages as in photon_paged_attention_decode_fp8.
  */
 int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const int32_t *block_tables,

@@ -22,11 +22,14 @@
 //  * q enters as f16 after an exact power-of-two scaling of its row to
 //    [1, 2), so any bf16 q keeps its 8 bits down to 2^-14 of the row's largest
 //    value; the factor goes into the score scale, the scale's sign into q.
-//  * Weights are kept relative to 2^(m + E - 8), m within 2^6 of the largest
-//    score so far and E the largest exponent of a V scale: a weight times its V
-//    scale then lies below 2^15 whatever the values' magnitude, and rounds to
-//    f16 with relative error 2^-12 down to 2^-22 of the largest, by at most
-//    2^-33 of it below.  For an fp32 output the remainder of that rounding
+//  * Weights and their sum are kept relative to 2^m, m at most 2^6 above the
+//    largest score so far, and so at most 1.  The weights of the second product
+//    take their V scale times 2^(14 - E), E the largest exponent of the V scales
+//    of the same 64 dims so far: they lie below 2^15 whatever the values'
+//    magnitude, and round to f16 with relative error 2^-12 down to 2^-22 of the
+//    largest, by at most 2^-33 of it below.  The accumulators carry 2^(14 - E)
+//    to the end of the item, the sum never: a V scale that dwarfs the earlier
+//    ones moves no weight.  For an fp32 output the remainder of the rounding
 //    follows in a second MMA (SPLIT); for a bf16 output (half a step: 2^-8) it
 //    would be lost anyway.  Sums, maxima and accumulators are fp32.
 //
@@ -47,12 +50,20 @@
 namespace photon {
 namespace {
 
-// Least exponent of the V scales that P follows: p is then at most 2^104 and
-// its sum over a context stays in fp32.
-constexpr int kFp4MinExp = -90;
-// Base-2 distance that a score may pass the reference maximum by before the
-// reference moves: a weight times its V scale stays below 2^15 either way.
+// Least E: 2^(14 - E) and its inverse are normal fp32 numbers.
+constexpr int kFp4MinExp = -112;
+// Base-2 distance of a new reference above the largest score: scores may grow
+// by as much before it moves again.
 constexpr float kFp4Slack = 6.f;
+// E is held as the bits of the least bf16 with a greater exponent.
+__device__ __forceinline__ uint32_t fp4_exp_limit(int e) { return static_cast<uint32_t>(e + 128) << 7; }
+// 2^(14 - E), and its inverse
+__device__ __forceinline__ float fp4_scale_down(uint32_t limit) {
+  return __uint_as_float((static_cast<uint32_t>(127 + 14 + 128) << 23) - (limit << 16));
+}
+__device__ __forceinline__ float fp4_scale_up(uint32_t limit) {
+  return __uint_as_float((limit << 16) - (static_cast<uint32_t>(128 + 14 - 127) << 23));
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -260,11 +271,11 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     for (int hh = 0; hh < HH; ++hh)
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) o[hh][mt][0] = o[hh][mt][1] = o[hh][mt][2] = o[hh][mt][3] = 0.f;
-    // weights are kept relative to m_ref; m_lim, e_lim: the largest scores and
-    // bits of a V scale that need no new reference
-    float m_lim[2] = {-INFINITY, -INFINITY}, m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    int e_run = kFp4MinExp;
-    uint32_t e_lim = 0;
+    // weights are kept relative to m_ref, no score's exceeding it; e_lim: E of each plane
+    float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    uint32_t e_lim[HH];
+#pragma unroll
+    for (int hh = 0; hh < HH; ++hh) e_lim[hh] = fp4_exp_limit(kFp4MinExp);
 
     while (w.page < w.n_pages && !gave_up) {
       const bool landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[c_slot], c_phase, kWaitBudgetCycles));
@@ -333,7 +344,9 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
           }
         }
         float m0 = fmaxf(x[0][0], x[0][2]), m1 = fmaxf(x[0][1], x[0][3]);
-        uint32_t sm = sv[0][0][0];
+        uint32_t sm[HH];
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh) sm[hh] = max_bf16x2(sv[0][hh][0], sv[0][hh][1]);
 #pragma unroll
         for (int i = 0; i < PP; ++i) {
           if (i > 0) {
@@ -341,40 +354,49 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
             m1 = max3(m1, x[i][1], x[i][3]);
           }
 #pragma unroll
-          for (int hh = 0; hh < HH; ++hh) sm = max_bf16x2(sm, max_bf16x2(sv[i][hh][0], sv[i][hh][1]));
+          for (int hh = 0; hh < HH; ++hh)
+            if (i > 0) sm[hh] = max_bf16x2(sm[hh], max_bf16x2(sv[i][hh][0], sv[i][hh][1]));
         }
-        sm = max(sm & 0xffffu, sm >> 16);
-        // The reference moves only when a score passes it by more than
-        // kFp4Slack or a V scale's exponent passes e_run (scales are not negative).
-        if (__any_sync(0xffffffffu, m0 * sl[0] > m_lim[0] || m1 * sl[1] > m_lim[1] || sm >= e_lim)) {
+        bool moves = m0 * sl[0] > m_ref[0] || m1 * sl[1] > m_ref[1];
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh) {
+          sm[hh] = max(sm[hh] & 0xffffu, sm[hh] >> 16);  // scales are not negative
+          moves |= sm[hh] >= e_lim[hh];
+        }
+        // A reference moves only when a score passes it or a V scale's exponent passes E.
+        if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
           }
-          const int es = static_cast<int>(__reduce_max_sync(0xffffffffu, sm) >> 7) - 127;
-          e_run = max(e_run, min(es, 127));
-          e_lim = static_cast<uint32_t>(e_run + 128) << 7;
           float alpha[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float m_run = fmaxf(m_lim[j] - kFp4Slack, (j ? m1 : m0) * sl[j]);
-            m_lim[j] = m_run + kFp4Slack;
-            const float ref = m_run + (static_cast<float>(e_run) - (14.f - kFp4Slack));
+            const float ref = fmaxf(m_ref[j] - kFp4Slack, (j ? m1 : m0) * sl[j]) + kFp4Slack;
             alpha[j] = exp2_approx(m_ref[j] - ref);
             m_ref[j] = ref;
             l_run[j] *= alpha[j];
           }
 #pragma unroll
-          for (int hh = 0; hh < HH; ++hh)
+          for (int hh = 0; hh < HH; ++hh) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, sm[hh]) >> 7;  // 127 + exponent
+            const uint32_t lim = max(e_lim[hh], fp4_exp_limit(min(static_cast<int>(top) - 127, 127)));
+            // 2^(old E - new E), 0 where that is below 2^-126
+            const float fall = __int_as_float(max(0x3f800000 - static_cast<int>((lim - e_lim[hh]) << 16), 0));
+            e_lim[hh] = lim;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-              o[hh][mt][0] *= alpha[0];
-              o[hh][mt][1] *= alpha[1];
-              o[hh][mt][2] *= alpha[0];
-              o[hh][mt][3] *= alpha[1];
+              o[hh][mt][0] *= alpha[0] * fall;
+              o[hh][mt][1] *= alpha[1] * fall;
+              o[hh][mt][2] *= alpha[0] * fall;
+              o[hh][mt][3] *= alpha[1] * fall;
             }
+          }
         }
+        float down[HH];
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh) down[hh] = fp4_scale_down(e_lim[hh]);
         uint32_t ph[PP][HH][2], pl[SPLIT ? PP : 1][HH][2];
 #pragma unroll
         for (int i = 0; i < PP; ++i)
@@ -386,7 +408,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
             l_run[1] += p1;
 #pragma unroll
             for (int hh = 0; hh < HH; ++hh) {
-              const float s = __uint_as_float(__byte_perm(sv[i][hh][n], 0u, half_sel));
+              const float s = __uint_as_float(__byte_perm(sv[i][hh][n], 0u, half_sel)) * down[hh];
               const float w0 = p0 * s, w1 = p1 * s;
               const uint32_t h = pack_half2(w0, w1);
               ph[i][hh][n] = transpose_8x8(h);
@@ -425,6 +447,8 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
       }
     }
 
+#pragma unroll
+    for (int i = 0; i < HH * 16; ++i) o[i / 16][i / 4 % 4][i % 4] *= fp4_scale_up(e_lim[i / 16]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll

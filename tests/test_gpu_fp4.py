@@ -607,3 +607,77 @@ def test_large_pool_offsets():
     ref = fp4.paged_attention(q, small, np.arange(4, dtype=np.int32)[None], ctx, 0.1)
     assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, 0.1, False, ref)).all()
     assert pk.photon_device_errors() == 0
+
+
+def _raise_v_scales(pool, bt, s, tokens, exps, plane=None):
+    """Multiplies the V scales of `tokens` of sequence s by 2^exps (None: makes
+    them 0), in every plane or in one; in place."""
+    byte, nib, sb = fp4.record_positions(pool.shape[-1] // 17)
+    for p, e in zip(tokens, exps):
+        rec = pool[bt[s, p // 16]]
+        at = sb[1, p % 16] if plane is None else sb[1, p % 16, plane:plane + 1]
+        bits = rec[:, at].astype(np.int64) | (rec[:, at + 1].astype(np.int64) << 8)
+        bits = np.zeros_like(bits) if e is None else bits + (e << 7)
+        rec[:, at], rec[:, at + 1] = bits & 0xFF, bits >> 8
+
+
+# one warp's steps in turn; a team's shares; split pieces; teams of pieces; long steps
+GROWING = [([48, 33, 35], 512, None), ([64, 500, 130], 512, None), ([300, 200, 90], 32, None),
+           ([3000, 700, 1500], 512, None), ([700, 33, 90, 1500], 64, 192 * 16 * 160)]
+
+
+@pytest.mark.parametrize("ctx,part,bound", GROWING)
+@pytest.mark.parametrize("early,late", [(None, 40), (None, 110), (-100, 40), (0, 60), (40, None), (110, -100)])
+@pytest.mark.parametrize("H,G,d", [(2, 4, 64), (2, 2, 128)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_decode_of_values_that_grow_or_vanish(ctx, part, bound, early, late, H, G, d, out):
+    """Values of one magnitude in a context's first tokens and of another in
+    the rest: no magnitude of a value changes how much a token's score counts."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(sum(ctx) + d)
+    mc = max(ctx) if bound is None else -(-bound // (len(ctx) * H) // 16) * 16
+    nb = sum(-(-c // 16) for c in ctx) + 1
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb, width=-(-mc // 16))
+    for s, c in enumerate(ctx):
+        cut = min(32, c - 1) if c < 64 else c // 2
+        _raise_v_scales(pool, bt, s, range(c), [early if p < cut else late for p in range(c)])
+    q, qt = _storage(rng.standard_normal((len(ctx), H * G, d)) * 0.1, "bf16")
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    got = _decode(pk, qt, _dev(pool), bt, ctx, d ** -0.5, dt, part, max_ctx=mc).double().cpu().numpy()
+    kd, vd = fp4.dequant(pool, d)
+    for s, c in enumerate(ctx):
+        one = fp4.paged_attention(q[s:s + 1], pool, bt[s:s + 1], [c], d ** -0.5)
+        mine = vd[bt[s, :-(-c // 16)]].transpose(0, 2, 1, 3).reshape(-1, H, d)[:c]
+        tol = _tolerance(oracle.to_f64(q), kd, mine, [c], d ** -0.5, out == "bf16", one)
+        assert (np.abs(got[s:s + 1] - one) <= tol).all()
+    assert pk.photon_device_errors() == 0
+
+
+@pytest.mark.parametrize("part", [32, 512])
+@pytest.mark.parametrize("exp", [40, -60, 100])
+def test_decode_planes_of_different_magnitude(part, exp):
+    """Each 64 dims have scales of their own: large ones in one plane leave the
+    other plane's outputs as exact as they were."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(part)
+    ctx, H, G, d, nb = [300, 40, 1, 700], 2, 4, 128, 70
+    pool = _random_pool(rng, nb, H, d)
+    bt = _tables(rng, ctx, nb)
+    for s, c in enumerate(ctx):
+        _raise_v_scales(pool, bt, s, range(c), [exp] * c, plane=0)
+    q, qt = _storage(rng.standard_normal((4, H * G, d)), "bf16")
+    for dt in (torch.bfloat16, torch.float32):
+        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.1, dt, part).double().cpu().numpy()
+        ref = fp4.paged_attention(q, pool, bt, ctx, 0.1)
+        kd, vd = fp4.dequant(pool, d)
+        live = np.zeros((nb, 16), bool)
+        for s, c in enumerate(ctx):
+            for p in range(c):
+                live[bt[s, p // 16], p % 16] = True
+        for x in (slice(0, 64), slice(64, 128)):
+            vx = np.where(live[:, None, :, None], vd, 0.0)[..., x]
+            tol = _tolerance(oracle.to_f64(q), kd, vx, ctx, 0.1, dt is torch.bfloat16, ref[..., x])
+            assert (np.abs(got[..., x] - ref[..., x]) <= tol).all()
