@@ -540,8 +540,11 @@ int photon_build_step_metadata(int32_t num_seqs, const int32_t *num_computed_tok
  * The pool is a stack, free_blocks[0 .. num_free - 1], its last entry handed
  * out first.  Released blocks are pushed first, in order of sequence and row;
  * then blocks are taken in order of sequence and row -- what
- * photon_block_pool_free and photon_build_step_metadata would do.
- *   free_blocks   int32 [num_blocks] (in/out; entries past num_free are written by releases)
+ * photon_block_pool_free and photon_build_step_metadata would do, but for one
+ * check: nothing on the device records which blocks are handed out, so a block
+ * released twice (held by two rows, or on the stack already) is not noticed
+ * unless the stack would grow past num_blocks.
+ *   free_blocks   int32 [num_blocks] (in/out; entries past num_free are written by releases, a refused step's too)
  *   num_free      int32 [1]; num_free_out int32 [1], may be the same address
  *   token_seq, positions, slot_mapping  [max_tokens] outputs; entries past the
  *                 step's tokens are 0, -1 and -1: the cache writes skip such a
@@ -550,11 +553,12 @@ int photon_build_step_metadata(int32_t num_seqs, const int32_t *num_computed_tok
  *   totals        int32 [4] output: tokens, longest context, free blocks left, status
  * The lengths are checked on the device.  A step that the host call would
  * refuse (a negative computed length, a row wider than max_blocks_per_seq, more
- * than max_tokens tokens: PHOTON_ERR_INVALID_ARG; too few free blocks:
- * PHOTON_ERR_POOL_EXHAUSTED) leaves block_tables, free_blocks and the pool as
- * they were, sets totals[3] to that status and PHOTON_DEVERR_METADATA, and
+ * than max_tokens tokens, a released row with a block id outside the pool:
+ * PHOTON_ERR_INVALID_ARG, the last with PHOTON_DEVERR_BLOCK_RANGE as well; too
+ * few free blocks: PHOTON_ERR_POOL_EXHAUSTED) leaves block_tables, the stack
+ * (free_blocks[0 .. num_free - 1]) and its count as they were, sets totals[3] to that status and PHOTON_DEVERR_METADATA, and
  * emits an empty step (no tokens, all contexts 0).  A block id outside the
- * pool gives its tokens slot -1 and sets PHOTON_DEVERR_BLOCK_RANGE.
+ * pool that a row grows by, or holds where its new tokens go, gives its tokens slot -1 and sets PHOTON_DEVERR_BLOCK_RANGE.
  * block_size 16; num_seqs <= 16384 and num_seqs * max_blocks_per_seq < 2^31
  * (PHOTON_ERR_UNSUPPORTED otherwise).
  */

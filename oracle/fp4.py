@@ -125,6 +125,9 @@ def step_metadata(nc, nn, tables, stack, max_tokens, num_blocks):
         tokens += max(int(n), 0)
         blocks += need - have if n >= 0 else 0
     released = sum(-(-int(c) // 16) for c, n in zip(nc, nn) if n < 0 and c >= 0)
+    for s in range(B if not bad else 0):        # what goes back to the pool must come from it
+        if nn[s] < 0:
+            bad |= any(not 0 <= int(x) < num_blocks for x in bt[s, :-(-int(nc[s]) // 16)])
     bad |= tokens > max_tokens or len(st) + released > num_blocks
     status = -1 if bad else (-5 if blocks > len(st) + released else 0)
     seq, pos, slots = [], [], []

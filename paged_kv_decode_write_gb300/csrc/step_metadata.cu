@@ -14,8 +14,11 @@
 //
 // One cluster of up to sixteen CTAs: every CTA computes all sums itself (reading
 // 8 bytes per sequence) and takes its share of the flat loops, so the only
-// exchange is one cluster barrier between the pushes onto the stack and the
-// reads from it.  The loops' searches and loads are latency, not bandwidth:
+// exchange is a cluster barrier between the pushes onto the stack and the reads
+// from it, and behind it one word per CTA: whether its share of the released
+// rows names a block outside the pool.  The barriers are passed whatever the
+// step holds, so CTAs that saw different lengths (changed under the kernel)
+// still meet.  The loops' searches and loads are latency, not bandwidth:
 // kMetaBatch entries of a thread run at once.
 //
 // The kernel never lets a dependent grid start early: the decode kernels read
@@ -61,8 +64,22 @@ __device__ __forceinline__ int warp_owner(const int32_t *off, int n, int x, int 
   }
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
+}
+
+// A word of the same place in another CTA's shared memory.
+__device__ __forceinline__ int cluster_load(const int *mine, int cta) {
+  unsigned at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(mine)), "r"(cta));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ unsigned long long scan_warp(unsigned long long v, int lane) {
@@ -102,12 +119,12 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
   const int B = a.num_seqs;
   int32_t *tok = offs, *gro = offs + B, *rel = offs + 2 * B;
   __shared__ unsigned long long wsum[2][32];
-  __shared__ int s_max, s_bad;
+  __shared__ int s_max, s_bad, s_foreign;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int warps = static_cast<int>(blockDim.x >> 5);
   const int gtid = blockIdx.x * blockDim.x + tid, threads = gridDim.x * blockDim.x;
   pdl_wait();
-  if (tid == 0) s_max = s_bad = 0;
+  if (tid == 0) s_max = s_bad = s_foreign = 0;
   __syncthreads();
 
   // ---- prefix sums (tokens in one word; grown and released blocks in
@@ -159,22 +176,34 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
     status = PHOTON_ERR_INVALID_ARG;
   else if (A > nf + R)
     status = PHOTON_ERR_POOL_EXHAUSTED;
-  const bool ok = status == PHOTON_OK;
-  const int T = ok ? static_cast<int>(total) : 0;
   __syncthreads();  // the sums
 
-  // ---- released blocks go on the stack, their row entries back to -1
-  if (ok)
+  // ---- released blocks go above the stack: cells that nothing holds yet, so a
+  // block from outside the pool can still refuse the step
+  const bool sound = status != PHOTON_ERR_INVALID_ARG;
+  if (sound)
     for (int j = gtid; j < R; j += threads) {
       const int s = owner(rel, B, j);
-      int32_t *entry = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s]);
-      const int32_t id = *entry;
-      if (id < 0 || id >= a.num_blocks) atomicOr(err, PHOTON_DEVERR_BLOCK_RANGE);
+      const int32_t id = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s])];
+      if (id < 0 || id >= a.num_blocks) s_foreign = 1;
       a.free_blocks[nf + j] = id;
-      *entry = -1;
     }
   // the stack is complete, and every CTA has read the lengths' sums and the count
   if (gridDim.x > 1) cluster_sync(); else __syncthreads();
+  bool foreign = false;
+  if (sound && R > 0)
+    foreign = gridDim.x > 1 ? __any_sync(0xffffffffu, lane < static_cast<int>(gridDim.x) &&
+                                                          cluster_load(&s_foreign, lane) != 0)
+                            : s_foreign != 0;
+  if (gridDim.x > 1) cluster_arrive();  // this CTA's reads are done; waited for at the end
+  if (foreign) status = PHOTON_ERR_INVALID_ARG;
+  const bool ok = status == PHOTON_OK;
+  const int T = ok ? static_cast<int>(total) : 0;
+  if (ok)
+    for (int j = gtid; j < R; j += threads) {
+      const int s = owner(rel, B, j);
+      a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s])] = -1;
+    }
   const int32_t *top = a.free_blocks + (nf + R - 1);  // the next block handed out
 
   // ---- grown blocks
@@ -240,8 +269,9 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
     a.totals[2] = left;
     a.totals[3] = status;
     *a.num_free_out = left;
-    if (!ok) atomicOr(err, PHOTON_DEVERR_METADATA);
+    if (!ok) atomicOr(err, PHOTON_DEVERR_METADATA | (foreign ? PHOTON_DEVERR_BLOCK_RANGE : 0u));
   }
+  if (gridDim.x > 1) cluster_wait();  // no CTA leaves while another may read its word
   __threadfence();  // a dependent grid may read these before its own dependency wait
 }
 

@@ -327,3 +327,54 @@ def test_a_step_that_takes_the_last_blocks(B, grown):
     dev.check(want)
     assert (room[:128] == 2 ** 30).all() and (room[128 + nb:] == 2 ** 30).all()
     assert pk.photon_device_errors() == 0
+
+
+@pytest.mark.parametrize("B", [4, 300, 5000])
+@pytest.mark.parametrize("bad", [-1, -7, "num_blocks", 2 ** 31 - 1])
+@pytest.mark.parametrize("where", ["first", "last", "middle", "exhausted"])
+def test_released_rows_with_foreign_blocks_are_refused(B, bad, where):
+    """As photon_block_pool_free refuses such an id: nothing changes, whichever
+    row and whichever CTA's share it lies in; the step without that row goes on."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(B)
+    W, nb, M = 4, B * 4 + 3, 3 * B
+    nc, tables, stack = _start(rng, B, W, nb, 1.0)
+    nc = np.maximum(nc, 1)
+    for s in range(B):
+        if tables[s, 0] < 0:
+            tables[s, 0] = stack.pop()
+    nn = np.where(rng.random(B) < 0.5, -1, 1).astype(np.int32)
+    nn[[0, B // 2, B - 1]] = -1
+    row = {"first": 0, "last": B - 1, "middle": B // 2, "exhausted": B // 2}[where]
+    if where == "exhausted":                     # too few blocks besides: the id is named first
+        stack = stack[:0]
+        nn[1] = 4 * 16 - nc[1]
+        M = 70 + 3 * B
+    good = tables.copy()
+    at = int(rng.integers(0, -(-int(nc[row]) // 16)))
+    tables[row, at] = nb if bad == "num_blocks" else bad
+    dev = Dev(tables, stack, nb, M)
+    free0 = dev.free.clone()
+    pk.photon_device_errors()
+    dev.step(pk, nc, nn)
+    assert pk.photon_device_errors() == pk.DEVERR_METADATA | pk.DEVERR_BLOCK_RANGE
+    assert dev.totals.tolist() == [0, 0, len(stack), -1]
+    assert np.array_equal(dev.tables.cpu().numpy(), tables)
+    assert torch.equal(dev.free[:len(stack)], free0[:len(stack)])
+    want = fp4.step_metadata(nc, nn, tables, stack, M, nb)
+    assert want[-1] == -1
+    dev.check(want)
+    nn[row] = 0                                   # the rest of the step, the row kept
+    want = fp4.step_metadata(nc, nn, tables, stack, M, nb)
+    dev.step(pk, nc, nn)
+    dev.check(want)
+    if want[-1] == 0:
+        assert all(0 <= x < nb for x in want[1])
+        assert pk.photon_device_errors() == 0
+    tables = good
+    dev = Dev(tables, stack, nb, M)               # and the sound row is released
+    nn[row] = -1
+    dev.step(pk, nc, nn)
+    dev.check(fp4.step_metadata(nc, nn, tables, stack, M, nb))
+    pk.photon_device_errors()
