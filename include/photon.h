@@ -392,8 +392,10 @@ size_t photon_kv_cache_fp4_record_bytes(int32_t head_dim);
 /*
  * photon_kv_cache_write_fp4 -- the batched RoPE-fused write into a 4-bit pool.
  * For every token with slot >= 0 and every KV head, y = RoPE(k) (v as it is),
- * the rotation rounded to fp32 and then to in_dtype (before those within about
- * 2^-36 of the exact one, relative to the pair); per 64 dims
+ * the rotation rounded to fp32 and then to in_dtype.  Before those, a rotated
+ * value is within 2^-34 times its pair's length (lengths above 2^-100) of the
+ * exact one, the angle within 2^-50 of positions[t] * theta^(-2i/d), relatively.
+ * Per 64 dims
  *   scale = bf16(max |y| / 6)   (the fp32 quotient, both to nearest-even)
  *   code  = nearest E2M1 of y / scale, halves to the even code, |code| <= 6
  * A group of zeros has scale 0; one that holds an infinity or a NaN has a NaN
