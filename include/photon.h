@@ -561,6 +561,9 @@ int photon_build_step_metadata(int32_t num_seqs, const int32_t *num_computed_tok
  * (free_blocks[0 .. num_free - 1]) and its count as they were, sets totals[3] to that status and PHOTON_DEVERR_METADATA, and
  * emits an empty step (no tokens, all contexts 0).  A block id outside the
  * pool that a row grows by, or holds where its new tokens go, gives its tokens slot -1 and sets PHOTON_DEVERR_BLOCK_RANGE.
+ * A program that carries the lengths on from context_lens must not do so after
+ * a refused step, whose contexts are all 0 while the rows keep their blocks: its
+ * next num_computed_tokens[s] is totals[3] == 0 ? context_lens[s] : the old one.
  * block_size 16; num_seqs <= 16384 and num_seqs * max_blocks_per_seq < 2^31
  * (PHOTON_ERR_UNSUPPORTED otherwise).
  */

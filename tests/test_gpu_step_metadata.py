@@ -378,3 +378,61 @@ def test_released_rows_with_foreign_blocks_are_refused(B, bad, where):
     dev.step(pk, nc, nn)
     dev.check(fp4.step_metadata(nc, nn, tables, stack, M, nb))
     pk.photon_device_errors()
+
+
+def test_lengths_survive_a_refused_step():
+    """A captured step that advances its lengths on the GPU, only when the step
+    was not refused: after one that ran out of blocks and one too long for its
+    row, every row, block and length is there, and the decode goes on."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(14)
+    B, W, H, G, d, nb, M = 3, 6, 2, 2, 64, 8, 100
+    i32 = dict(dtype=torch.int32, device="cuda")
+    nc, nn = torch.zeros(B, **i32), torch.zeros(B, **i32)
+    k = torch.from_numpy(rng.standard_normal((M, H, d)).astype(np.float32)).bfloat16().cuda()
+    v = torch.from_numpy(rng.standard_normal((M, H, d)).astype(np.float32)).bfloat16().cuda()
+    q = torch.from_numpy(rng.standard_normal((B, H * G, d)).astype(np.float32)).bfloat16().cuda()
+    dev = Dev(np.full((B, W), -1, np.int32), list(range(nb)), nb, M)
+    pool = torch.zeros(nb, H, 17 * d, dtype=torch.uint8, device="cuda")
+    out = torch.empty(B, H * G, d, device="cuda")
+    ws = torch.empty(pk.photon_paged_attention_workspace_size(B, H * G, d, W * 16, 32), dtype=torch.uint8,
+                     device="cuda")
+
+    def step():
+        pk.photon_build_step_metadata_device(nc, nn, dev.tables, dev.free, dev.num_free, dev.seq, dev.pos, dev.slots,
+                                             dev.lens, dev.totals)
+        pk.photon_kv_cache_write_fp4(k, v, dev.pos, dev.slots, pool, 1e4)
+        pk.photon_paged_attention_decode_fp4(q, pool, dev.tables, dev.lens, 0.125, out, W * 16, 32, ws)
+        torch.where(dev.totals[3] == 0, dev.lens, nc, out=nc)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    tables, stack, host_nc = np.full((B, W), -1, np.int32), list(range(nb)), np.zeros(B, np.int32)
+    # 7 of 8 blocks; out of blocks; a row too long; one token each; the first released, the others grow
+    plan = [([30, 40, 20], 0), ([3, 9, 20], -5), ([0, 57, 0], -1), ([1, 1, 1], 0), ([-1, 30, 5], 0), ([9, 1, 1], 0)]
+    for new, status in plan:
+        nn.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = fp4.step_metadata(host_nc, new, tables, stack, M, nb)
+        assert want[-1] == status
+        dev.check(want)
+        if status:
+            assert (out == 0).all() and np.array_equal(nc.cpu().numpy(), host_nc)
+            continue
+        tables, stack, host_nc = want[0], want[1], want[5].astype(np.int32)
+        assert np.array_equal(nc.cpu().numpy(), host_nc)
+        p = pool.cpu().numpy()
+        ref = fp4.paged_attention(q.view(torch.int16).cpu().numpy().view(np.uint16), p, np.maximum(tables, 0),
+                                  host_nc, 0.125)
+        tol = _tolerance(q.double().cpu().numpy(), *fp4.dequant(p, d), host_nc, 0.125, False, ref)
+        assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    held = tables[tables >= 0].tolist()
+    assert sorted(held + stack) == list(range(nb))
+    assert pk.photon_device_errors() == pk.DEVERR_METADATA
