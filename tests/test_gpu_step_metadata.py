@@ -436,3 +436,20 @@ def test_lengths_survive_a_refused_step():
     held = tables[tables >= 0].tolist()
     assert sorted(held + stack) == list(range(nb))
     assert pk.photon_device_errors() == pk.DEVERR_METADATA
+
+
+def test_the_order_in_which_released_blocks_are_taken_again():
+    """The same step as test_released_blocks_are_taken_again_in_the_same_step,
+    against the result written out: [0, 1] + [4, 5, 6] + [2] is popped from its end."""
+    pk = ensure_built()
+    tables = np.array([[4, 5, 6], [-1, -1, -1], [2, -1, -1], [-1, -1, -1]], np.int32)
+    nc, nn = [48, 0, 3, 0], [-1, 30, -7, 40]
+    dev = Dev(tables, [0, 1], 7, 70)
+    dev.step(pk, nc, nn)
+    assert dev.tables.tolist() == [[-1, -1, -1], [2, 6, -1], [-1, -1, -1], [5, 4, 1]]
+    assert dev.free[:1].tolist() == [0] and dev.num_free.item() == 1
+    assert dev.totals.tolist() == [70, 40, 1, 0] and dev.lens.tolist() == [0, 30, 0, 40]
+    slots = [b * 16 + o for b in (2, 6) for o in range(16)][:30] + [b * 16 + o for b in (5, 4, 1) for o in range(16)][:40]
+    assert dev.slots.tolist() == slots
+    want = fp4.step_metadata(nc, nn, tables, [0, 1], 70, 7)
+    assert np.array_equal(want[0], dev.tables.cpu().numpy()) and want[1] == [0]
