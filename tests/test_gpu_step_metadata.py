@@ -453,3 +453,24 @@ def test_the_order_in_which_released_blocks_are_taken_again():
     assert dev.slots.tolist() == slots
     want = fp4.step_metadata(nc, nn, tables, [0, 1], 70, 7)
     assert np.array_equal(want[0], dev.tables.cpu().numpy()) and want[1] == [0]
+
+
+@pytest.mark.parametrize("release", [False, True])
+def test_as_many_sequences_as_a_step_takes(release):
+    """16384 sequences: the sums fill a CTA's shared memory, sixteen to a thread."""
+    pk = ensure_built()
+    rng = np.random.default_rng(16)
+    B, W = 16384, 3
+    nb = B * W + 5
+    nc, tables, stack = _start(rng, B, W, nb, 0.8)
+    nn = np.minimum(rng.choice([0, 1, 1, 1, 20], B), W * 16 - nc)
+    if release:
+        nn = np.where(rng.random(B) < 0.4, -1, nn)
+    M = int(np.maximum(nn, 0).sum()) + 3
+    dev = Dev(tables, stack, nb, M)
+    pk.photon_device_errors()
+    dev.step(pk, nc, nn)
+    want = fp4.step_metadata(nc, nn, tables, stack, M, nb)
+    assert want[-1] == 0
+    dev.check(want)
+    assert pk.photon_device_errors() == 0
