@@ -178,15 +178,18 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
     status = PHOTON_ERR_POOL_EXHAUSTED;
   __syncthreads();  // the sums
 
-  // ---- released blocks go above the stack: cells that nothing holds yet, so a
-  // block from outside the pool can still refuse the step
-  const bool sound = status != PHOTON_ERR_INVALID_ARG;
+  // ---- released blocks go above the stack, cells that nothing holds yet, and
+  // their row entries back to -1; a block from outside the pool refuses the step,
+  // and the entries return from those cells
+  const bool sound = status != PHOTON_ERR_INVALID_ARG, fits = status == PHOTON_OK;
   if (sound)
     for (int j = gtid; j < R; j += threads) {
       const int s = owner(rel, B, j);
-      const int32_t id = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s])];
+      int32_t *entry = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s]);
+      const int32_t id = *entry;
       if (id < 0 || id >= a.num_blocks) s_foreign = 1;
       a.free_blocks[nf + j] = id;
+      if (fits) *entry = -1;
     }
   // the stack is complete, and every CTA has read the lengths' sums and the count
   if (gridDim.x > 1) cluster_sync(); else __syncthreads();
@@ -199,10 +202,10 @@ __global__ void __launch_bounds__(kMetaThreads) step_metadata_kernel(const StepM
   if (foreign) status = PHOTON_ERR_INVALID_ARG;
   const bool ok = status == PHOTON_OK;
   const int T = ok ? static_cast<int>(total) : 0;
-  if (ok)
-    for (int j = gtid; j < R; j += threads) {
+  if (foreign && fits)
+    for (int j = gtid; j < R; j += threads) {  // the thread's own cells
       const int s = owner(rel, B, j);
-      a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s])] = -1;
+      a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + (j - rel[s])] = a.free_blocks[nf + j];
     }
   const int32_t *top = a.free_blocks + (nf + R - 1);  // the next block handed out
 
