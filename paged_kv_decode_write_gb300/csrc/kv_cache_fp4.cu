@@ -282,6 +282,7 @@ struct RowLoad {
 
 // One CTA per tile of tokens (all heads): the tile's rotation table in shared
 // memory, then rows (K or V, head, token), token fastest, D/16 lanes each.
+// Four CTAs per SM: at their 64 registers the fp32 kernels spill 36 bytes.
 template <typename Tag, int D>
 __global__ void __launch_bounds__(kFp4Threads, 4)
     kv_cache_write_fp4_kernel(const __grid_constant__ Fp4WriteArgs a, unsigned int *err) {

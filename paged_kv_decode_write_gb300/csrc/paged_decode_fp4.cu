@@ -34,10 +34,10 @@
 //    would be lost anyway.  Sums, maxima and accumulators are fp32.
 //
 // What bounds it: DRAM on long steps (with the merge, 128 contexts of up to 32k
-// tokens, d 64: 6.4 TB/s of records, 64 of d 128: 6.6; a copy reads and writes
-// 6.8), the issue slots right behind it (116 warp instructions per 1088-byte
+// tokens, d 64: 6.3 TB/s of records, 64 of d 128: 6.6; a copy reads and writes
+// 6.8), the issue slots right behind it (some 120 warp instructions per 1088-byte
 // page, ALU pipe 65 %, tensor pipe 32 %); start-up, uneven ends and the merge on
-// steps of some 30 pages per warp (64 ragged sequences of d 128: 4.1 TB/s);
+// steps of some 30 pages per warp (64 ragged sequences of d 128: 4.0 TB/s);
 // latency on single requests.
 #include <algorithm>
 #include <atomic>
