@@ -474,3 +474,70 @@ def test_as_many_sequences_as_a_step_takes(release):
     assert want[-1] == 0
     dev.check(want)
     assert pk.photon_device_errors() == 0
+
+
+@pytest.mark.parametrize("B,H,G,d,first", [(64, 8, 4, 64, 200), (300, 2, 4, 128, 40), (2, 8, 2, 128, 900)])
+@pytest.mark.parametrize("write", [False, True])
+def test_back_to_back_steps_read_the_metadata_of_their_own_step(B, H, G, d, first, write):
+    """Forty steps with no other kernel between them, streamed and captured:
+    each decode reads lengths and tables early, and the buffers it reads are
+    those that the decode two steps before it read with other contents."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(B)
+    steps, W = 40, -(-(first + 60) // 16)
+    nb = B * W
+    i32 = dict(dtype=torch.int32, device="cuda")
+    start = torch.from_numpy(rng.integers(first // 2, first, B).astype(np.int32)).cuda()
+    perm = torch.from_numpy(rng.permutation(nb).astype(np.int32)).cuda()
+    held = (start + 15) // 16
+    col = torch.arange(W, device="cuda")[None]
+    at = (held.cumsum(0) - held)[:, None] + col
+    tables0 = torch.where(col < held[:, None], perm[at.clamp(max=nb - 1)], -1).int()
+    used = int(held.sum())
+    free0 = torch.zeros(nb, **i32)
+    free0[:nb - used] = perm[used:]
+    pool0 = torch.randint(0, 256, (nb, H, 17 * d), dtype=torch.uint8, device="cuda")
+    byte, nib, sb = fp4.record_positions(d)
+    for w in range(2):                                   # scales in (0, 2)
+        pool0[:, :, sb[w].ravel() + 1] = 0x3E
+    rows = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).bfloat16().cuda()
+    k, v, q = rows(steps, B, H, d), rows(steps, B, H, d), rows(B, H * G, d)
+    one = torch.ones(B, **i32)
+    ws = torch.empty(max(1, pk.photon_paged_attention_workspace_size(B, H * G, d, W * 16, 64)), dtype=torch.uint8,
+                     device="cuda")
+    seq, pos = torch.empty(B, **i32), torch.empty(B, **i32)
+    slots, totals = torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty(4, **i32)
+    tables, free, count, pool = tables0.clone(), free0.clone(), torch.empty(1, **i32), pool0.clone()
+    lens = [torch.empty(B, **i32) for _ in range(2)]
+    out = torch.empty(steps, B, H * G, d, device="cuda")
+
+    def reset():
+        tables.copy_(tables0), free.copy_(free0), pool.copy_(pool0), count.fill_(nb - used), lens[1].copy_(start)
+        out.fill_(float("nan"))
+
+    def chain(sync):
+        for i in range(steps):
+            pk.photon_build_step_metadata_device(lens[(i + 1) % 2], one, tables, free, count, seq, pos, slots,
+                                                 lens[i % 2], totals)
+            sync()
+            if write:
+                pk.photon_kv_cache_write_fp4(k[i], v[i], pos, slots, pool, 1e4)
+                sync()
+            pk.photon_paged_attention_decode_fp4(q, pool, tables, lens[i % 2], 0.1, out[i], W * 16, 64, ws)
+            sync()
+
+    pk.photon_device_errors()
+    reset()
+    chain(torch.cuda.synchronize)
+    want = out.clone()
+    assert torch.isfinite(want).all() and (want[1:] != want[:-1]).any(-1).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for run in [lambda: chain(lambda: None)] * 5 + [graph.replay] * 5:
+        reset()
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert pk.photon_device_errors() == 0
