@@ -426,7 +426,8 @@ def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block
     into num_free_out if given); num_new_tokens[s] < 0 releases row s.  Fills
     token_seq, positions (int32) and slot_mapping (int64), all [max_tokens],
     context_lens int32 [B] and totals int32 [4] (tokens, longest context, free
-    blocks, status)."""
+    blocks, status).  A refused step (status not 0) has all contexts 0: carry
+    the lengths on only from steps whose status is 0."""
     B, W = block_tables.shape
     M, = token_seq.shape
     blocks, = free_blocks.shape

@@ -681,3 +681,28 @@ def test_decode_planes_of_different_magnitude(part, exp):
             vx = np.where(live[:, None, :, None], vd, 0.0)[..., x]
             tol = _tolerance(oracle.to_f64(q), kd, vx, ctx, 0.1, dt is torch.bfloat16, ref[..., x])
             assert (np.abs(got[..., x] - ref[..., x]) <= tol).all()
+
+
+@pytest.mark.parametrize("kexp", [116, 60, -60, -110])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("part", [32, 512])
+def test_decode_keys_of_any_magnitude(kexp, d, part):
+    """Keys up to just below 2^119 and down to 2^-112, the softmax scale
+    bringing their scores back to a few units."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(kexp + 200)
+    ctx, H, G, nb = [300, 40, 1], 2, 4, 30
+    pool = _random_pool(rng, nb, H, d)
+    byte, nib, sb = fp4.record_positions(d)
+    bits = (pool[:, :, sb[0]].astype(np.int64) | (pool[:, :, sb[0] + 1].astype(np.int64) << 8)) + (kexp << 7)
+    pool[:, :, sb[0]], pool[:, :, sb[0] + 1] = bits & 0xFF, bits >> 8
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((3, H * G, d)), "bf16")
+    kd, vd = fp4.dequant(pool, d)
+    assert np.abs(kd).max() < 2.0 ** 119
+    scale = float(np.float32(d ** -0.5 * 2.0 ** -kexp))
+    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, torch.float32, part).double().cpu().numpy()
+    ref = fp4.paged_attention(q, pool, bt, ctx, scale)
+    assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, scale, False, ref)).all()
+    assert pk.photon_device_errors() == 0
