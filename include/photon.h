@@ -447,6 +447,131 @@ int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const
                                       int32_t partition_size, photon_dtype out_dtype, void *workspace,
                                       size_t workspace_bytes, photon_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys (Qwen3-type attention), fused with rotation and write.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * photon_qk_norm_rope_kv_cache_write -- photon_rope_q_kv_cache_write with an
+ * RMS norm of every head of q and k before the rotation, in the same launch:
+ *   q[i][g][:]   = round(RoPE(N(q[i][g][:], q_weight), q_positions[i]))     in place
+ *   K of token t = round(RoPE(N(k[t][h][:], k_weight), positions[t]))       at its slot
+ *   V of token t = v[t][h][:]                                               (bit copy)
+ *   N(x, w)_e    = x_e w_e / sqrt(mean_e x_e^2 + eps)
+ * The mean square, the norm and the rotation are fp32, rounded once to kv_dtype:
+ * before that rounding a value is within 2^-19 times its normalised pair's length of the
+ * exact one.  The mean square must fit fp32 (|x| below 2^60).
+ *   q            device [num_q_tokens][num_q_heads][head_dim], kv_dtype, 16-B aligned;
+ *                may be NULL only when num_q_tokens is 0
+ *   q_weight, k_weight  device [head_dim], kv_dtype, 16-B aligned
+ *   eps          > 0, finite
+ * num_q_heads and num_kv_heads at most 4096 (PHOTON_ERR_UNSUPPORTED otherwise).
+ * Other arguments and errors as photon_rope_q_kv_cache_write.
+ */
+int photon_qk_norm_rope_kv_cache_write(void *q, const int32_t *q_positions, int32_t num_q_tokens,
+                                       int32_t num_q_heads, const void *k, const void *v,
+                                       const int32_t *positions, const int64_t *slot_mapping,
+                                       const void *q_weight, const void *k_weight, float eps, void *k_cache,
+                                       void *v_cache, int32_t num_tokens, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                       photon_dtype kv_dtype, float rope_theta, photon_rope rope_style,
+                                       photon_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit KV cache: integer codes of -127 .. 127 with one fp32 scale per block of
+ * 16 tokens, KV head and K or V, computed at the write: no calibration, and
+ * a block's scale follows its own tokens.
+ *
+ * Layout: one pool for K and V, uint8 [num_blocks][num_kv_heads][record],
+ * record = photon_kv_cache_int8_record_bytes(head_dim) = 32 * head_dim + 16
+ * bytes, head_dim 64 or 128.  Inside a record the codes (+ 128) lie in the order
+ * of the attention kernel's fragments (csrc/int8.cuh gives every byte), then
+ * the two scales.  value = code * scale.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of one (block, KV head) record; 0 for a head_dim without one. */
+size_t photon_kv_cache_int8_record_bytes(int32_t head_dim);
+
+/*
+ * photon_kv_cache_write_int8 -- the batched RoPE-fused write into an 8-bit pool.
+ * For the tokens that the call writes to a block, y = RoPE(k) (v as it is), the
+ * rotation in fp32; per block, KV head and K or V
+ *   m     = max |y| over the rows written
+ *   s     = the block's scale, 0 if the call writes the block's first token
+ *           (offset 0), which starts the block anew
+ *   s'    = s                        if fl(m / 127) <= s
+ *         = max(fl(m / 127), 2 s)    otherwise
+ *   code  = y * fl(1 / s') rounded to the nearest integer, halves to even
+ * Rows of the block that the call does not write keep their values, rounded
+ * to the new scale where it grew (code * fl(s * fl(1 / s')), halves to even: all
+ * such roundings of a row together stay within one step of its last scale), or
+ * become zero if the block starts anew.  So tokens have to arrive in order, as a
+ * sequence appends them; what a released block held before does not matter.
+ * A scale below 2^-100 counts as zero (the values read as 0).  A row that holds an
+ * infinity or a NaN gives its block (K or V, that head) a NaN scale until the block
+ * starts anew: all its tokens read back as NaN.
+ *   k, v      device [num_tokens][num_kv_heads][head_dim], in_dtype (f32 or bf16), 16-B aligned
+ *   kv_cache  device 8-bit pool, 16-B aligned
+ *   slot_mapping  distinct slots; the tokens of one block stand next to each
+ *             other, in any order, with nothing in between (lists by sequence and
+ *             position do).  Where they do not, the blocks concerned hold no
+ *             defined values
+ * head_dim 64 or 128, num_kv_heads <= 1024, num_blocks < 2^31
+ * (PHOTON_ERR_UNSUPPORTED otherwise; the same for the calls below).  Other
+ * arguments and errors as photon_kv_cache_write.
+ */
+int photon_kv_cache_write_int8(const void *k, const void *v, const int32_t *positions,
+                               const int64_t *slot_mapping, void *kv_cache, int32_t num_tokens,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                               int64_t num_blocks, photon_dtype in_dtype, float rope_theta,
+                               photon_rope rope_style, photon_stream_t stream);
+
+/*
+ * photon_qk_norm_rope_kv_cache_write_int8 -- photon_qk_norm_rope_kv_cache_write
+ * into an 8-bit pool: y = RoPE(N(k, k_weight)) in fp32, quantised as
+ * photon_kv_cache_write_int8 does, and q normalised and rotated in place
+ * (in_dtype), in one launch.
+ */
+int photon_qk_norm_rope_kv_cache_write_int8(void *q, const int32_t *q_positions, int32_t num_q_tokens,
+                                            int32_t num_q_heads, const void *k, const void *v,
+                                            const int32_t *positions, const int64_t *slot_mapping,
+                                            const void *q_weight, const void *k_weight, float eps,
+                                            void *kv_cache, int32_t num_tokens, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                            photon_dtype in_dtype, float rope_theta, photon_rope rope_style,
+                                            photon_stream_t stream);
+
+/*
+ * photon_kv_cache_read_int8 -- the cached rows of the tokens at slot_mapping,
+ * the fp32 product code * scale rounded to out_dtype: a prefix held in 8 bits that
+ * a bf16 prefill attends to.  K comes back rotated, as written.  Arguments as
+ * photon_kv_cache_read_fp4.
+ */
+int photon_kv_cache_read_int8(const void *kv_cache, const int64_t *slot_mapping, void *k, void *v,
+                              int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int64_t num_blocks, photon_dtype out_dtype,
+                              photon_stream_t stream);
+
+/*
+ * photon_paged_attention_decode_int8 -- photon_paged_attention_decode over an
+ * 8-bit pool: the same attention on the dequantised values.  q is bf16 (already
+ * rotated) of any magnitude.  The scores, softmax and sums are fp32; a softmax
+ * weight times its block's V scale enters the second product in f16 (11
+ * significant bits) for a bf16 output, as f16 and its f16 remainder (22) for an
+ * fp32 one, scaled by the largest V scale so far.  K and V may have any magnitude
+ * whose sums fit fp32: |k| below 2^110, |v| summed over a context below 2^127,
+ * |scale| times a row's largest |q| below 2^110, and the scores themselves.
+ * Workspace as for photon_paged_attention_decode; the split-K pieces are
+ * equal runs of pages as in photon_paged_attention_decode_fp8.
+ */
+int photon_paged_attention_decode_int8(const void *q, const void *kv_cache, const int32_t *block_tables,
+                                       const int32_t *context_lens, float scale, void *out,
+                                       int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                       int32_t max_blocks_per_seq, int32_t max_context_len,
+                                       int32_t partition_size, photon_dtype out_dtype, void *workspace,
+                                       size_t workspace_bytes, photon_stream_t stream);
+
 /*
  * Reads (and, if clear != 0, resets) the sticky PHOTON_DEVERR_* bits of the
  * current device.  Synchronises the device: a diagnostic, not a hot-path call.

@@ -25,6 +25,9 @@ __all__ = [
     "photon_paged_attention_decode_fp8", "photon_paged_attention_partial_fp8",
     "photon_kv_cache_fp4_record_bytes", "photon_kv_cache_write_fp4", "photon_kv_cache_read_fp4",
     "photon_paged_attention_decode_fp4", "photon_build_step_metadata_device",
+    "photon_qk_norm_rope_kv_cache_write", "photon_qk_norm_rope_kv_cache_write_int8",
+    "photon_kv_cache_int8_record_bytes", "photon_kv_cache_write_int8", "photon_kv_cache_read_int8",
+    "photon_paged_attention_decode_int8",
     "photon_paged_attention_prefill",
     "photon_paged_attention_workspace_size",
     "photon_paged_attention_decode", "photon_paged_attention_partial",
@@ -101,6 +104,19 @@ def lib() -> ctypes.CDLL:
     L.photon_paged_attention_decode_fp4.argtypes = [P, P, P, P, f32, P, i32, i32, i32, i32, i32, i64, i32,
                                                     i32, i32, E, P, sz, P]
     L.photon_paged_attention_decode_fp4.restype = E
+    norm = [P, P, i32, i32, P, P, P, P, P, P, f32]
+    L.photon_qk_norm_rope_kv_cache_write.argtypes = norm + [P, P, i32, i32, i32, i32, i64, E, f32, E, P]
+    L.photon_qk_norm_rope_kv_cache_write.restype = E
+    L.photon_qk_norm_rope_kv_cache_write_int8.argtypes = norm + [P, i32, i32, i32, i32, i64, E, f32, E, P]
+    L.photon_qk_norm_rope_kv_cache_write_int8.restype = E
+    L.photon_kv_cache_int8_record_bytes.argtypes = [i32]
+    L.photon_kv_cache_int8_record_bytes.restype = sz
+    for name in ("write", "read"):
+        f = getattr(L, f"photon_kv_cache_{name}_int8")
+        f.argtypes = getattr(L, f"photon_kv_cache_{name}_fp4").argtypes
+        f.restype = E
+    L.photon_paged_attention_decode_int8.argtypes = L.photon_paged_attention_decode_fp4.argtypes
+    L.photon_paged_attention_decode_int8.restype = E
     L.photon_build_step_metadata_device.argtypes = [P, P, i32, i32, P, i32, P, i64, P, P, i32, P, P, P, P,
                                                     P, P]
     L.photon_build_step_metadata_device.restype = E
@@ -361,10 +377,10 @@ def _rows(what, t):
     return shape
 
 
-def _pool(kv_cache, H, d, dev, dtype):
-    shape = kv_cache.shape
-    if len(shape) != 3 or shape[1] != H or shape[2] != 17 * d:
-        raise ValueError(f"kv_cache must be [num_blocks, {H}, {17 * d}], got {tuple(shape)}")
+def _pool(kv_cache, H, d, dev, dtype, record=None):
+    shape, record = kv_cache.shape, 17 * d if record is None else record
+    if len(shape) != 3 or shape[1] != H or shape[2] != record:
+        raise ValueError(f"kv_cache must be [num_blocks, {H}, {record}], got {tuple(shape)}")
     return _arg("kv_cache", kv_cache, dtype, None, dev), shape[0]
 
 
@@ -396,25 +412,129 @@ def photon_kv_cache_read_fp4(kv_cache, slot_mapping, k, v, stream=None):
         _arg("v", v, dtype, shape, dev), T, H, d, 16, nb, _dt(k), st), "photon_kv_cache_read_fp4")
 
 
-def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
-                                      partition_size=512, workspace=None, stream=None):
-    """Decode attention over a 4-bit pool (see photon_kv_cache_write_fp4); q
-    bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
+def _decode_record_args(q, kv_cache, block_tables, context_lens, scale, out, max_context_len, partition_size,
+                        workspace, stream, record):
+    """Arguments of a decode over a pool of records of record(head_dim) bytes."""
     shape = _rows("q", q)
     B, Hq, d = shape
     torch, dev, st = _place("q", q, stream)
     Hkv, W = kv_cache.shape[1], block_tables.shape[1]
-    pool, nb = _pool(kv_cache, Hkv, d, dev, torch.uint8)
+    pool, nb = _pool(kv_cache, Hkv, d, dev, torch.uint8, record(d))
     if workspace is None:
         ws, ws_bytes = None, 0
     else:
         ws = _arg("workspace", workspace, workspace.dtype, None, dev)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().photon_paged_attention_decode_fp4(
-        _arg("q", q, torch.bfloat16, None, dev), pool, _arg("block_tables", block_tables, torch.int32, (B, W), dev),
-        _arg("context_lens", context_lens, torch.int32, (B,), dev), float(scale), _arg("out", out, out.dtype, shape, dev),
-        B, Hq, Hkv, d, 16, nb, W, int(max_context_len), int(partition_size), _dt(out), ws, ws_bytes, st),
-        "photon_paged_attention_decode_fp4")
+    return (_arg("q", q, torch.bfloat16, None, dev), pool,
+            _arg("block_tables", block_tables, torch.int32, (B, W), dev),
+            _arg("context_lens", context_lens, torch.int32, (B,), dev), float(scale),
+            _arg("out", out, out.dtype, shape, dev), B, Hq, Hkv, d, 16, nb, W, int(max_context_len),
+            int(partition_size), _dt(out), ws, ws_bytes, st)
+
+
+def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
+                                      partition_size=512, workspace=None, stream=None):
+    """Decode attention over a 4-bit pool (see photon_kv_cache_write_fp4); q
+    bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
+    _check(lib().photon_paged_attention_decode_fp4(*_decode_record_args(
+        q, kv_cache, block_tables, context_lens, scale, out, max_context_len, partition_size, workspace, stream,
+        lambda d: 17 * d)), "photon_paged_attention_decode_fp4")
+
+
+# ---- q/k norms in the write, 8-bit KV cache with a scale per block and head ------
+
+def _norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight):
+    """The leading arguments of the writes with norms (q and its companions None:
+    no query rows)."""
+    shape, dtype = _rows("k", k), k.dtype
+    T, H, d = shape
+    i32 = torch.int32
+    if q is None:
+        head = (None, None, 0, 0)
+        qw = None
+    else:
+        Tq, Hq, dq = _rows("q", q)
+        if dq != d:
+            raise ValueError(f"q must have head_dim {d}, got {dq}")
+        head = (_arg("q", q, dtype, None, dev), _arg("q_positions", q_positions, i32, (Tq,), dev), Tq, Hq)
+        qw = _arg("q_weight", q_weight, dtype, (d,), dev)
+    return head + (_arg("k", k, dtype, None, dev), _arg("v", v, dtype, shape, dev),
+                   _arg("positions", positions, i32, (T,), dev),
+                   _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), qw,
+                   _arg("k_weight", k_weight, dtype, (d,), dev))
+
+
+def photon_qk_norm_rope_kv_cache_write(q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight, eps,
+                                       k_cache, v_cache, rope_theta, rope_style="neox", stream=None):
+    """RMS norms of q [Tq, H_q, d] (weights q_weight [d]) and k [T, H_kv, d]
+    (k_weight [d]) per head, their rotation, and the write of k and v; q in
+    place.  All of one type, float32 or bfloat16; q None: keys only."""
+    T, H, d = _rows("k", k)
+    torch, dev, st = _place("k", k, stream)
+    shape, dtype = k_cache.shape, k.dtype
+    if len(shape) != 4 or shape[1] != H or shape[3] != d:
+        raise ValueError(f"k_cache must be [num_blocks, {H}, block_size, {d}], got {tuple(shape)}")
+    style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
+    _check(lib().photon_qk_norm_rope_kv_cache_write(
+        *_norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight), float(eps),
+        _arg("k_cache", k_cache, dtype, None, dev), _arg("v_cache", v_cache, dtype, shape, dev), T, H, d, shape[2],
+        shape[0], _dt(k), float(rope_theta), style, st), "photon_qk_norm_rope_kv_cache_write")
+
+
+def photon_kv_cache_int8_record_bytes(head_dim: int) -> int:
+    """Bytes of one (block, KV head) record of an 8-bit pool (0: no such head_dim)."""
+    return int(lib().photon_kv_cache_int8_record_bytes(int(head_dim)))
+
+
+def photon_kv_cache_write_int8(k, v, positions, slot_mapping, kv_cache, rope_theta, rope_style="neox",
+                               stream=None):
+    """8-bit write with a scale per block and head: k, v [T, H_kv, d] (float32 or
+    bfloat16); positions int32 [T]; slot_mapping int64 [T], the tokens of a block
+    next to each other; kv_cache uint8 [num_blocks, H_kv, 32 * d + 16]."""
+    shape, dtype = _rows("k", k), k.dtype
+    T, H, d = shape
+    torch, dev, st = _place("k", k, stream)
+    pool, nb = _pool(kv_cache, H, d, dev, torch.uint8, 32 * d + 16)
+    style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
+    _check(lib().photon_kv_cache_write_int8(
+        _arg("k", k, dtype, None, dev), _arg("v", v, dtype, shape, dev),
+        _arg("positions", positions, torch.int32, (T,), dev),
+        _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), pool, T, H, d, 16, nb, _dt(k), float(rope_theta),
+        style, st), "photon_kv_cache_write_int8")
+
+
+def photon_qk_norm_rope_kv_cache_write_int8(q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight, eps,
+                                            kv_cache, rope_theta, rope_style="neox", stream=None):
+    """photon_qk_norm_rope_kv_cache_write into an 8-bit pool (see
+    photon_kv_cache_write_int8)."""
+    T, H, d = _rows("k", k)
+    torch, dev, st = _place("k", k, stream)
+    pool, nb = _pool(kv_cache, H, d, dev, torch.uint8, 32 * d + 16)
+    style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
+    _check(lib().photon_qk_norm_rope_kv_cache_write_int8(
+        *_norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight), float(eps), pool,
+        T, H, d, 16, nb, _dt(k), float(rope_theta), style, st), "photon_qk_norm_rope_kv_cache_write_int8")
+
+
+def photon_kv_cache_read_int8(kv_cache, slot_mapping, k, v, stream=None):
+    """Dequantised rows of the tokens at slot_mapping (int64 [T]) into k and v
+    [T, H_kv, d] (float32 or bfloat16)."""
+    shape, dtype = _rows("k", k), k.dtype
+    T, H, d = shape
+    torch, dev, st = _place("k", k, stream)
+    pool, nb = _pool(kv_cache, H, d, dev, torch.uint8, 32 * d + 16)
+    _check(lib().photon_kv_cache_read_int8(
+        pool, _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), _arg("k", k, dtype, None, dev),
+        _arg("v", v, dtype, shape, dev), T, H, d, 16, nb, _dt(k), st), "photon_kv_cache_read_int8")
+
+
+def photon_paged_attention_decode_int8(q, kv_cache, block_tables, context_lens, scale, out, max_context_len,
+                                       partition_size=512, workspace=None, stream=None):
+    """Decode attention over an 8-bit pool (see photon_kv_cache_write_int8); q
+    bfloat16 [B, H_q, d], out [B, H_q, d] (float32 or bfloat16)."""
+    _check(lib().photon_paged_attention_decode_int8(*_decode_record_args(
+        q, kv_cache, block_tables, context_lens, scale, out, max_context_len, partition_size, workspace, stream,
+        lambda d: 32 * d + 16)), "photon_paged_attention_decode_int8")
 
 
 def photon_build_step_metadata_device(num_computed_tokens, num_new_tokens, block_tables, free_blocks, num_free,

@@ -63,8 +63,37 @@ struct Fp4WriteArgs {
   unsigned long long turns[64];
 };
 
-// Read of 4-bit cache rows back to a floating type.
-struct Fp4ReadArgs {
+// The writes with q/k norms (bf16 / fp32 caches) and the 8-bit writes: angles as
+// fractions of a turn (times 2^64); the launcher fills the fields from `q_tiles` on.
+struct NormRopeArgs {
+  void *q;  // rows normalised and rotated in place; NULL with no query tokens
+  const int32_t *q_positions;
+  const void *q_weight;
+  const void *k;
+  const void *v;
+  const int32_t *positions;
+  const int64_t *slot_mapping;
+  const void *k_weight;
+  void *k_cache;  // 8-bit: the record pool
+  void *v_cache;
+  int64_t num_slots;
+  int32_t num_q_tokens;
+  int32_t num_q_heads;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t rope_style;
+  float eps;
+  uint32_t q_div;   // 2^28 / heads, rounded up: row / heads = row * div >> 28
+  uint32_t kv_div;
+  unsigned long long turns[kMaxRopePairs];
+  int32_t q_tiles;  // CTAs that take query tiles (the first ones)
+  int32_t q_tile_log2;
+  int32_t tile_log2;
+};
+constexpr int kNormMaxHeads = 4096;  // (8 tokens x heads)^2 < 2^28 / 8 keeps that division exact
+
+// Read of 4-bit and 8-bit cache rows back to a floating type.
+struct CacheReadArgs {
   const void *pool;
   const int64_t *slot_mapping;
   void *k_out;
@@ -174,10 +203,19 @@ cudaError_t launch_decode_partial_fp8(const DecodeArgs &a, const float *k_scale,
                                       const float *v_scale, unsigned int *err, cudaStream_t st);
 cudaError_t launch_kv_cache_write_fp4(const WriteArgs &a, photon_dtype in_dt, unsigned int *err,
                                       cudaStream_t st);
-cudaError_t launch_kv_cache_read_fp4(const Fp4ReadArgs &a, photon_dtype out_dt, unsigned int *err,
+cudaError_t launch_kv_cache_read_fp4(const CacheReadArgs &a, photon_dtype out_dt, unsigned int *err,
                                      cudaStream_t st);
 cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st);
 cudaError_t launch_decode_merge_fp4(const DecodeArgs &a, cudaStream_t st);
+// log2 of a CTA's tokens, at most `most`: as many as leave two CTAs per SM.
+int norm_tile_log2(int64_t tokens, int most);
+cudaError_t launch_qk_norm_rope_write(NormRopeArgs a, photon_dtype dt, int head_dim, unsigned int *err,
+                                      cudaStream_t st);
+cudaError_t launch_kv_cache_write_int8(NormRopeArgs a, bool norm, photon_dtype in_dt, int head_dim,
+                                       unsigned int *err, cudaStream_t st);
+cudaError_t launch_kv_cache_read_int8(const CacheReadArgs &a, photon_dtype out_dt, unsigned int *err,
+                                      cudaStream_t st);
+cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st);
 cudaError_t launch_step_metadata(const StepMetaArgs &a, unsigned int *err, cudaStream_t st);
 
 // Every host-side check of photon_paged_attention_decode except the workspace

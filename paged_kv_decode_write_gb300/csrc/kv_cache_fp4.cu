@@ -16,6 +16,7 @@
 #include <cmath>
 
 #include "fp4.cuh"
+#include "row_lanes.cuh"
 
 namespace photon {
 namespace {
@@ -253,33 +254,6 @@ __device__ __forceinline__ uint32_t quant_word(const float (&x)[8], uint32_t sbi
   return cvt_e2m1x8(y);
 }
 
-// A lane's 16 values of a row as loaded: dims 8w .. 8w + 7 and those + D/2.
-template <typename T>
-struct RowLoad {
-  static constexpr int N = sizeof(T) / 2;
-  uint4 lo[N], hi[N];
-  __device__ __forceinline__ void load(const T *src, int half) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      lo[i] = reinterpret_cast<const uint4 *>(src)[i];
-      hi[i] = reinterpret_cast<const uint4 *>(src + half)[i];
-    }
-  }
-  __device__ __forceinline__ static void widen(const uint4 (&r)[N], float (&x)[8]) {
-    if constexpr (N == 1) {
-      Unpack<BF16Tag>::run(r[0], x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[4 * i] = __uint_as_float(r[i].x);
-        x[4 * i + 1] = __uint_as_float(r[i].y);
-        x[4 * i + 2] = __uint_as_float(r[i].z);
-        x[4 * i + 3] = __uint_as_float(r[i].w);
-      }
-    }
-  }
-};
-
 // One CTA per tile of tokens (all heads): the tile's rotation table in shared
 // memory, then rows (K or V, head, token), token fastest, D/16 lanes each.
 // Four CTAs per SM: at their 64 registers the fp32 kernels spill 36 bytes.
@@ -373,27 +347,12 @@ __global__ void __launch_bounds__(kFp4Threads, 4)
 
 // ---- read --------------------------------------------------------------------------
 
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-  uint4 w;
-  uint32_t *u = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t *>(&b);
-  }
-  *reinterpret_cast<uint4 *>(p) = w;
-}
-
 // One CTA per (tile of consecutive tokens, KV head): tokens of one page then
 // share the sectors they read.  A lane takes the same 8 dims of a token's K and
 // V, so that the slot's arithmetic serves two words.
 template <typename Tag, int D>
 __global__ void __launch_bounds__(kFp4Threads)
-    kv_cache_read_fp4_kernel(const Fp4ReadArgs a, int tile, unsigned int *err) {
+    kv_cache_read_fp4_kernel(const CacheReadArgs a, int tile, unsigned int *err) {
   using T = typename Tag::T;
   constexpr int LANES = D / 8;  // of a token
   pdl_wait();
@@ -451,7 +410,7 @@ cudaError_t launch_write(const Fp4WriteArgs &a, unsigned int *err, cudaStream_t 
 }
 
 template <typename Tag>
-cudaError_t launch_read(const Fp4ReadArgs &a, unsigned int *err, cudaStream_t st) {
+cudaError_t launch_read(const CacheReadArgs &a, unsigned int *err, cudaStream_t st) {
   using T = typename Tag::T;
   // 64 tokens per CTA where that leaves eight CTAs per SM, else 16
   const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + 63) / 64 * a.num_kv_heads;
@@ -461,7 +420,7 @@ cudaError_t launch_read(const Fp4ReadArgs &a, unsigned int *err, cudaStream_t st
   // the grid's y extent is at most 65535 tiles: longer reads in pieces
   constexpr int64_t kMaxTiles = 65535;
   for (int64_t t = 0; t < tiles; t += kMaxTiles) {
-    Fp4ReadArgs p = a;
+    CacheReadArgs p = a;
     const int64_t first = t * tile, offset = first * a.num_kv_heads * a.head_dim;
     p.slot_mapping = a.slot_mapping + first;
     p.k_out = static_cast<T *>(a.k_out) + offset;
@@ -502,7 +461,7 @@ cudaError_t launch_kv_cache_write_fp4(const WriteArgs &wa, photon_dtype in_dt, u
   return in_dt == PHOTON_BF16 ? launch_write<BF16Tag>(a, err, st) : launch_write<F32Tag>(a, err, st);
 }
 
-cudaError_t launch_kv_cache_read_fp4(const Fp4ReadArgs &a, photon_dtype out_dt, unsigned int *err,
+cudaError_t launch_kv_cache_read_fp4(const CacheReadArgs &a, photon_dtype out_dt, unsigned int *err,
                                      cudaStream_t st) {
   if (a.num_tokens == 0) return cudaSuccess;
   return out_dt == PHOTON_BF16 ? launch_read<BF16Tag>(a, err, st) : launch_read<F32Tag>(a, err, st);

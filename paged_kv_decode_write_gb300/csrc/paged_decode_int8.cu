@@ -1,0 +1,502 @@
+// Split-K paged decode attention over the 8-bit KV cache with one scale per block
+// and KV head, head_dim 64 or 128, on the tensor cores.  Record layout in
+// int8.cuh; partial / merge contract, work split and walker as the FP8 and 4-bit
+// kernels' (paged_decode_mma.cuh).
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(x_j - m),  x_j = scale log2(e) s_K <q, c_j>
+//
+//  * A record is contiguous and in fragment order: a page is one bulk copy into
+//    the warp's shared-memory ring and every fragment conflict-free 16-byte loads.
+//    The lanes that hold a step's block-table entries issue its copies, ST steps
+//    of PP pages ahead of the arithmetic and across item boundaries.
+//  * S = K Q^T with the 16 tokens of a page as the MMA's rows and up to 8 query
+//    heads as its columns; O^T = V^T P^T takes P through one movmatrix per 8 tokens.
+//  * A byte b becomes the f16 number 1024 + b by a byte permute (0x64 into the high
+//    byte) and the code by subtracting 1152, exactly: a permute and a half of an
+//    f16x2 subtraction per pair of K codes, one logic operation more per pair of V
+//    codes, whose bytes lie token by token.  The scales never touch a code: s_K
+//    multiplies a page's scores, s_V its weights.
+//  * q enters as f16 after an exact power-of-two scaling of its row to [1, 2), so
+//    any bf16 q keeps its 8 bits down to 2^-14 of the row's largest value.
+//  * Weights and their sum are kept relative to 2^m, m at most 2^6 above the
+//    largest score so far.  The weights of the second product take s_V 2^(14 - E),
+//    E the largest exponent of the item's s_V so far: below 2^15 whatever the
+//    values' magnitude, rounded to f16 with relative error 2^-12 down to 2^-22 of
+//    the largest; the accumulators carry 2^(14 - E) to the end of the item, the sum
+//    never.  For an fp32 output the remainder of that rounding follows in a second
+//    MMA (SPLIT).  Sums, maxima and accumulators are fp32.
+#include <algorithm>
+#include <atomic>
+
+#include "int8.cuh"
+#include "mma_f16.cuh"
+#include "paged_decode.cuh"
+#include "paged_decode_mma.cuh"
+
+namespace photon {
+namespace {
+
+// Least E: 2^(14 - E) and its inverse are normal fp32 numbers.
+constexpr int kMinExp = -112;
+// Base-2 distance of a new reference above the largest score.
+constexpr float kSlack = 6.f;
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+constexpr uint32_t kHalf1024 = 0x64646464u;  // high byte of an f16 in [1024, 2048)
+constexpr uint32_t kHalf1152 = 0x64806480u;  // 1152 twice
+
+// The four codes of a word as f16: (byte 0, byte 1) and (byte 2, byte 3).
+__device__ __forceinline__ void codes_in_order(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  lo = sub_f16x2(__byte_perm(w, kHalf1024, 0x4140u), kHalf1152);
+  hi = sub_f16x2(__byte_perm(w, kHalf1024, 0x4342u), kHalf1152);
+}
+
+// Byte i of a and of b as f16 codes (a in the low half).
+template <int I>
+__device__ __forceinline__ uint32_t codes_across(uint32_t a, uint32_t b) {
+  const uint32_t w = __byte_perm(a, b, 0x0400u + 0x0101u * I);
+  return sub_f16x2((w & 0x00ff00ffu) | 0x64006400u, kHalf1152);
+}
+
+// Stage ring of a warp: ST steps of PP pages, whole records.
+template <int D, int PP, int ST, int NW>
+struct Int8Ring {
+  static constexpr int REC = int8_record_bytes(D);
+  static constexpr int STAGE = PP * REC;
+  static constexpr int SMEM = NW * ST * (STAGE + 8);
+  static_assert(32 % PP == 0, "a step lies in one block-table window");
+  static_assert(ST * PP <= 32, "a bit per page of the ring");
+};
+
+// TEAM: an item belongs to a CTA, whose warps take a share of its pages each
+// and meet in shared memory at its end (else every warp has items of its own).
+// They walk the same items, so their barriers match; a warp that gave up on a
+// copy still walks on to them.
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, bool TEAM>
+__global__ void __launch_bounds__(NW * 32, MIN_CTAS)
+    paged_decode_int8_kernel(const DecodeArgs a, unsigned int *err) {
+  using R = Int8Ring<D, PP, ST, NW>;
+  constexpr int HH = D / 64;
+  constexpr int REC = R::REC;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int G = a.num_q_heads / a.num_kv_heads;
+  unsigned char *stages = smem + warp * ST * R::STAGE;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NW * ST * R::STAGE) + warp * ST;
+  if (lane == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(&bars[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if constexpr (BAL) prefetch_tables_l2(a);
+  pdl_launch_dependents();
+  const uint64_t policy = l2_evict_first_policy();
+  const int workers = gridDim.x * (TEAM ? 1 : NW);  // that take items
+
+  // this warp's share of an item's pages: whole steps, in order
+  auto share = [&](Walker &w) {
+    if constexpr (TEAM) {
+      const int part = ((w.n_pages + NW - 1) / NW + PP - 1) / PP * PP;
+      const int lo = min(warp * part, w.n_pages);
+      w.n_pages = min(part, w.n_pages - lo);
+      w.pg0 += lo;
+    }
+  };
+  auto next_item = [&](Walker &w) {
+    walker_next<BAL>(w, a, lane, err, workers);
+    if (w.valid) share(w);
+  };
+  Walker prod, w;  // the producer, ST steps ahead, and the consumer
+  walker_start<BAL>(prod, a, lane, err, TEAM ? blockIdx.x : blockIdx.x * NW + warp, workers);
+  if (prod.valid) share(prod);
+  w = prod;
+
+  // Block-table window of the producer's item: lane j holds the record row of
+  // page 32 k + j, `there` which of them exist with a block id in the pool;
+  // the next window's ids are on their way.
+  uint32_t there = 0, valid_bits = 0;
+  int64_t row = 0;
+  int ahead = -1, c_slot = 0;
+  uint32_t c_phase = 0;
+  auto table_entry = [&](int page) -> int {
+    return page < prod.n_pages
+               ? a.block_tables[seq_table_row(a, prod.s) * a.max_blocks_per_seq + prod.pg0 + page]
+               : -1;
+  };
+  if (prod.valid) ahead = table_entry(lane);
+  // metadata only so far; pages, q and the workspace wait for the preceding kernel
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.seg_count)  // the merge's mode
+    a.seg_count[static_cast<int64_t>(a.num_seqs) * a.num_q_heads] = BAL ? 1 : 0;
+
+  // Starts the copies of the producer's next step into ring slot `slot`: the
+  // lanes of its pages in the window each copy their record.  False past the
+  // warp's last step.
+  auto issue_next = [&](int slot) -> bool {
+    while (prod.valid && prod.page >= prod.n_pages) {
+      next_item(prod);
+      if (prod.valid) ahead = table_entry(lane);
+    }
+    if (!prod.valid) return false;
+    const int at = prod.page & 31;
+    if (at == 0) {
+      const bool in = prod.page + lane < prod.n_pages;
+      const bool ok = in && ahead >= 0 && ahead < a.num_blocks;
+      row = ok ? static_cast<int64_t>(ahead) * a.num_kv_heads + prod.h : 0;
+      there = __ballot_sync(0xffffffffu, ok);
+      if (in && !ok) atomicOr(err, PHOTON_DEVERR_BLOCK_RANGE);
+      ahead = table_entry(prod.page + 32 + lane);
+    }
+    const uint32_t v = (there >> at) & ((1u << PP) - 1);
+    valid_bits = (valid_bits & ~(((1u << PP) - 1) << (PP * slot))) | (v << (PP * slot));
+    if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(v) * REC);
+    const int i = lane - at;
+    if (i >= 0 && i < PP && (v >> i & 1u)) {
+      fence_proxy_async_smem();
+      bulk_copy_g2s(stages + slot * R::STAGE + i * REC,
+                    static_cast<const unsigned char *>(a.k_cache) + row * REC, REC, &bars[slot], policy);
+    }
+    prod.page += PP;
+    return true;
+  };
+#pragma unroll 1
+  for (int k = 0; k < ST; ++k)
+    if (!issue_next(k)) break;
+
+  bool gave_up = false;
+  __shared__ float team_o[TEAM ? NW - 1 : 1][HH * 16][32];  // of warps 1 ..: accumulators,
+  __shared__ float team_ml[TEAM ? NW - 1 : 1][4][32];       // references and sums
+  while (w.valid) {
+    // ---- a new item: the query group
+    uint32_t qb[HH][4][2];     // q of head g, dims 16c + 4kt + {0,1}, {2,3} of each plane
+    float sl[2];               // score factor of heads 2c, 2c + 1
+    {
+      float f[HH][16], qm = 0.f;
+#pragma unroll
+      for (int hh = 0; hh < HH; ++hh)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (g < G)
+            v = reinterpret_cast<const uint4 *>(
+                static_cast<const __nv_bfloat16 *>(a.q) +
+                (static_cast<int64_t>(w.s) * a.num_q_heads + w.h * G + g) * D + 64 * hh + 16 * c)[i];
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[hh][8 * i + 2 * j] = bf16_lo(u[j]);
+            f[hh][8 * i + 2 * j + 1] = bf16_hi(u[j]);
+            qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(u[j])), fabsf(bf16_hi(u[j]))));
+          }
+        }
+      qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 1));
+      qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 2));
+      int e = static_cast<int>(__float_as_uint(qm) >> 23) - 127;
+      if (e == 128 || qm == 0.f) e = 0;
+      e = max(e, -100);
+      const float down = e == 127 ? 0x1p-127f : pow2(-e);  // 2^-e
+      const float s = a.scale_log2 * pow2(e);
+      sl[0] = __shfl_sync(0xffffffffu, s, 8 * c);
+      sl[1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
+#pragma unroll
+      for (int hh = 0; hh < HH; ++hh)
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          qb[hh][kt][0] = pack_half2(f[hh][4 * kt] * down, f[hh][4 * kt + 1] * down);
+          qb[hh][kt][1] = pack_half2(f[hh][4 * kt + 2] * down, f[hh][4 * kt + 3] * down);
+        }
+    }
+    float o[HH][4][4];         // O^T: dims 64 hh + 8g + 2mt + {0, 1} of heads 2c, 2c + 1
+#pragma unroll
+    for (int hh = 0; hh < HH; ++hh)
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) o[hh][mt][0] = o[hh][mt][1] = o[hh][mt][2] = o[hh][mt][3] = 0.f;
+    // weights are kept relative to m_ref, no score's exceeding it; E: see above
+    float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    int E = kMinExp;
+
+    while (w.page < w.n_pages && !gave_up) {
+      const bool landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[c_slot], c_phase, kWaitBudgetCycles));
+      if (!landed) {
+        if (lane == 0) atomicOr(err, PHOTON_DEVERR_WAIT_TIMEOUT);
+        drain_async_copies();
+        if constexpr (!TEAM) return;
+        gave_up = true;  // the team's other warps still wait for this one
+        break;
+      }
+      const uint32_t valid = (valid_bits >> (PP * c_slot)) & ((1u << PP) - 1);
+      const unsigned char *stage = stages + c_slot * R::STAGE;
+      // ---- scores: x[i][2n + j] belongs to token 4 (g >> 1) + 2n + (g & 1) of page i, head 2c + j
+      float x[PP][4], sv[PP];
+#pragma unroll
+      for (int i = 0; i < PP; ++i) {
+        float acc[4];
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh) {
+          const uint4 r0 = *reinterpret_cast<const uint4 *>(stage + i * REC + 1024 * hh + 16 * lane);
+          const uint4 r1 = *reinterpret_cast<const uint4 *>(stage + i * REC + 1024 * hh + 512 + 16 * lane);
+          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) {
+            uint32_t a0, a1, a2, a3;
+            codes_in_order(w0[kt], a0, a2);
+            codes_in_order(w1[kt], a1, a3);
+            if (hh == 0 && kt == 0)
+              mma_f16_first(acc, a0, a1, a2, a3, qb[hh][kt][0], qb[hh][kt][1]);
+            else
+              mma_f16(acc, a0, a1, a2, a3, qb[hh][kt][0], qb[hh][kt][1]);
+          }
+        }
+        const float2 sc = *reinterpret_cast<const float2 *>(stage + i * REC + int8_scale_byte(D, 0));
+        const float f0 = sl[0] * sc.x, f1 = sl[1] * sc.x;
+        x[i][0] = acc[0] * f0;
+        x[i][1] = acc[1] * f1;
+        x[i][2] = acc[2] * f0;
+        x[i][3] = acc[3] * f1;
+        sv[i] = sc.y;
+      }
+      const int tok0 = (w.pg0 + w.page) * kBlockSize;
+      w.page += PP;
+      if (valid) {  // no page of the step in the pool: nothing to add
+        // tokens past the context, of absent pages: weight 0 (their bytes may hold anything)
+        if (valid != (1u << PP) - 1 || tok0 + PP * kBlockSize > w.tok1) {
+#pragma unroll
+          for (int i = 0; i < PP; ++i) {
+            const int nv = (valid >> i & 1u) ? w.tok1 - (tok0 + i * kBlockSize) : 0;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              if (4 * (g >> 1) + 2 * n + (g & 1) >= nv) x[i][2 * n] = x[i][2 * n + 1] = -INFINITY;
+            if (nv <= 0) sv[i] = 0.f;
+          }
+        }
+        float m0 = fmaxf(x[0][0], x[0][2]), m1 = fmaxf(x[0][1], x[0][3]);
+        uint32_t top = __float_as_uint(sv[0]);
+#pragma unroll
+        for (int i = 1; i < PP; ++i) {
+          m0 = max3(m0, x[i][0], x[i][2]);
+          m1 = max3(m1, x[i][1], x[i][3]);
+          top = max(top, __float_as_uint(sv[i]));
+        }
+        const int e_top = min(static_cast<int>(top >> 23 & 0xffu) - 127, 127);  // the same in every lane
+        // A reference moves only when a score passes it or a V scale's exponent passes E.
+        if (__any_sync(0xffffffffu, m0 > m_ref[0] || m1 > m_ref[1] || e_top > E)) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          float alpha[2];
+          const int e_new = max(E, e_top);
+          const float fall = pow2(max(E - e_new, -127));  // 0 below 2^-126
+          E = e_new;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float ref = fmaxf(m_ref[j] - kSlack, j ? m1 : m0) + kSlack;
+            alpha[j] = exp2_approx(m_ref[j] - ref);
+            m_ref[j] = ref;
+            l_run[j] *= alpha[j];
+            alpha[j] *= fall;
+          }
+#pragma unroll
+          for (int hh = 0; hh < HH; ++hh)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              o[hh][mt][0] *= alpha[0];
+              o[hh][mt][1] *= alpha[1];
+              o[hh][mt][2] *= alpha[0];
+              o[hh][mt][3] *= alpha[1];
+            }
+        }
+        const float down = pow2(14 - E);
+        uint32_t ph[PP][2], pl[SPLIT ? PP : 1][2];
+#pragma unroll
+        for (int i = 0; i < PP; ++i) {
+          const float s = sv[i] * down;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = exp2_approx(x[i][2 * n] - m_ref[0]);
+            const float p1 = exp2_approx(x[i][2 * n + 1] - m_ref[1]);
+            l_run[0] += p0;
+            l_run[1] += p1;
+            const float w0 = p0 * s, w1 = p1 * s;
+            const uint32_t h = pack_half2(w0, w1);
+            ph[i][n] = transpose_8x8(h);
+            if constexpr (SPLIT) {
+              const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+              pl[i][n] = transpose_8x8(pack_half2(w0 - r.x, w1 - r.y));
+            }
+          }
+        }
+        // ---- O^T += V^T P^T: bytes of the same dim of two tokens make an f16 pair of the A operand
+#pragma unroll
+        for (int i = 0; i < PP; ++i)
+#pragma unroll
+          for (int hh = 0; hh < HH; ++hh) {
+            const unsigned char *vp = stage + i * REC + 16 * D + 1024 * hh + 16 * lane;
+            const uint4 v0 = *reinterpret_cast<const uint4 *>(vp);        // tokens 4c, 4c + 1
+            const uint4 v1 = *reinterpret_cast<const uint4 *>(vp + 512);  // tokens 4c + 2, 4c + 3
+            auto tile = [&](float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+              mma_f16(acc, a0, a1, a2, a3, ph[i][0], ph[i][1]);
+              if constexpr (SPLIT) mma_f16(acc, a0, a1, a2, a3, pl[i][0], pl[i][1]);
+            };
+            tile(o[hh][0], codes_across<0>(v0.x, v0.z), codes_across<1>(v0.x, v0.z),
+                 codes_across<0>(v1.x, v1.z), codes_across<1>(v1.x, v1.z));
+            tile(o[hh][1], codes_across<2>(v0.x, v0.z), codes_across<3>(v0.x, v0.z),
+                 codes_across<2>(v1.x, v1.z), codes_across<3>(v1.x, v1.z));
+            tile(o[hh][2], codes_across<0>(v0.y, v0.w), codes_across<1>(v0.y, v0.w),
+                 codes_across<0>(v1.y, v1.w), codes_across<1>(v1.y, v1.w));
+            tile(o[hh][3], codes_across<2>(v0.y, v0.w), codes_across<3>(v0.y, v0.w),
+                 codes_across<2>(v1.y, v1.w), codes_across<3>(v1.y, v1.w));
+          }
+      }
+      __syncwarp();  // the stage is read before the next copies overwrite it
+      issue_next(c_slot);
+      if (++c_slot == ST) {
+        c_slot = 0;
+        c_phase ^= 1u;
+      }
+    }
+
+    const float up = pow2(E - 14);
+#pragma unroll
+    for (int i = 0; i < HH * 16; ++i) o[i / 16][i / 4 % 4][i % 4] *= up;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], d);
+    if constexpr (TEAM) {  // warp 0 adds the others' shares, in order
+      if (warp > 0) {
+#pragma unroll
+        for (int i = 0; i < HH * 16; ++i) team_o[warp - 1][i][lane] = o[i / 16][i / 4 % 4][i % 4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          team_ml[warp - 1][j][lane] = m_ref[j];
+          team_ml[warp - 1][2 + j][lane] = l_run[j];
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {
+        float M[2] = {m_ref[0], m_ref[1]}, f[NW][2];
+#pragma unroll
+        for (int k = 0; k < NW - 1; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) M[j] = fmaxf(M[j], team_ml[k][j][lane]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f[0][j] = m_ref[j] == -INFINITY ? 0.f : exp2_approx(m_ref[j] - M[j]);
+          l_run[j] *= f[0][j];
+          m_ref[j] = M[j];
+        }
+#pragma unroll
+        for (int k = 0; k < NW - 1; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float mk = team_ml[k][j][lane];
+            f[k + 1][j] = mk == -INFINITY ? 0.f : exp2_approx(mk - M[j]);
+            l_run[j] = fmaf(team_ml[k][2 + j][lane], f[k + 1][j], l_run[j]);
+          }
+#pragma unroll
+        for (int i = 0; i < HH * 16; ++i) {
+          float &y = o[i / 16][i / 4 % 4][i % 4];
+          y *= f[0][i & 1];
+#pragma unroll
+          for (int k = 0; k < NW - 1; ++k) y = fmaf(team_o[k][i][lane], f[k + 1][i & 1], y);
+        }
+      }
+      __syncthreads();  // read before the next item's shares are written
+      if (warp > 0) {
+        next_item(w);
+        continue;
+      }
+    }
+    // ---- item done: o[hh][mt][2r + j] is head 2c + j, dim 64 hh + 8g + 2mt + r
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float l = l_run[j];
+      const int head = 2 * c + j;
+      if (head >= G) continue;
+      const int64_t qrow = static_cast<int64_t>(w.s) * a.num_q_heads + w.h * G + head;
+      if constexpr (BAL)
+        if (g == 0 && w.p == 0) a.seg_count[qrow] = w.P_s;
+      const bool whole = w.P_s == 1;
+      const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const int64_t prow = qrow * a.max_partitions + w.p;
+#pragma unroll
+      for (int hh = 0; hh < HH; ++hh) {
+        float v[8];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          v[2 * mt] = o[hh][mt][j] * f;
+          v[2 * mt + 1] = o[hh][mt][2 + j] * f;
+        }
+        if (whole && a.out_bf16) {
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + qrow * D + 64 * hh + 8 * g) =
+              make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                         pack_bf16(v[6], v[7]));
+        } else {
+          float *dst = (whole ? static_cast<float *>(a.out) + qrow * D : a.o_part + prow * D) + 64 * hh + 8 * g;
+          reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
+      if (!whole && g == 0) {
+        a.m_part[prow] = m_ref[j];
+        a.l_part[prow] = l;
+      }
+    }
+    next_item(w);
+  }
+}
+
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT>
+cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
+  constexpr int SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
+  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, false>;
+  static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  int occ = occupancy[dev].load(std::memory_order_relaxed);
+  if (occ == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, NW * 32, SMEM);
+    if (e != cudaSuccess) return e;
+    occ = occ > 0 ? occ : 1;
+    occupancy[dev].store(occ, std::memory_order_relaxed);
+  }
+  const int64_t items = static_cast<int64_t>(a.num_seqs) * a.max_partitions * a.num_kv_heads;
+  if (items == 0) return cudaSuccess;
+  const int64_t workers = std::min(items, static_cast<int64_t>(device_sm_count()) * occ * NW);
+  DecodeArgs la = a;
+  la.balanced = BAL ? 1 : 0;
+  return launch_pdl(kern, dim3(static_cast<unsigned>((workers + NW - 1) / NW)), dim3(NW * 32), SMEM, stream, la, err);
+}
+
+template <int D, int PP, int ST, int MIN_CTAS>
+cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
+  if (balanced_pieces(a))
+    return a.out_bf16 ? launch_int8_kern<D, PP, ST, 4, MIN_CTAS, true, false>(a, err, st)
+                      : launch_int8_kern<D, PP, ST, 4, MIN_CTAS, true, true>(a, err, st);
+  return a.out_bf16 ? launch_int8_kern<D, PP, ST, 4, MIN_CTAS, false, false>(a, err, st)
+                    : launch_int8_kern<D, PP, ST, 4, MIN_CTAS, false, true>(a, err, st);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
+  if (a.head_dim == 64) return launch_int8<64, 2, 3, 4>(a, err, st);
+  if (a.head_dim == 128) return launch_int8<128, 1, 3, 3>(a, err, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace photon

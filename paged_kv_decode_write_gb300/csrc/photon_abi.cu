@@ -561,6 +561,16 @@ int photon_device_errors(uint32_t *flags_out, int clear) {
 namespace photon {
 namespace {
 
+// theta^(-2 (8 j + k) / d) as a product of two powers: 12 or 16 of them, not 32 or 64 (1 us of the call)
+void frequencies(float theta, int head_dim, double *inv_freq) {
+  double fine[8];
+  for (int k = 0; k < 8; ++k) fine[k] = std::pow(static_cast<double>(theta), -2.0 * k / head_dim);
+  for (int j = 0; j < head_dim / 16; ++j) {
+    const double coarse = std::pow(static_cast<double>(theta), -16.0 * j / head_dim);
+    for (int k = 0; k < 8; ++k) inv_freq[8 * j + k] = coarse * fine[k];
+  }
+}
+
 // Shape checks shared by the 4-bit calls (record pool of num_blocks blocks).
 int check_fp4_pool(int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks) {
   if (num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PHOTON_ERR_INVALID_ARG;
@@ -611,13 +621,7 @@ int photon_kv_cache_write_fp4(const void *k, const void *v, const int32_t *posit
   a.num_kv_heads = num_kv_heads;
   a.head_dim = head_dim;
   a.rope_style = rope_style;
-  // theta^(-2 (8 j + k) / d) as a product of two powers: 12 or 16 of them, not 32 or 64 (1 us of the call)
-  double fine[8];
-  for (int k = 0; k < 8; ++k) fine[k] = std::pow(static_cast<double>(rope_theta), -2.0 * k / head_dim);
-  for (int j = 0; j < head_dim / 16; ++j) {
-    const double coarse = std::pow(static_cast<double>(rope_theta), -16.0 * j / head_dim);
-    for (int k = 0; k < 8; ++k) a.inv_freq[8 * j + k] = coarse * fine[k];
-  }
+  photon::frequencies(rope_theta, head_dim, a.inv_freq);
   unsigned int *err = error_word();
   if (!err) return PHOTON_ERR_CUDA;
   return cuda_status(launch_kv_cache_write_fp4(a, in_dtype, err, reinterpret_cast<cudaStream_t>(stream)));
@@ -634,7 +638,7 @@ int photon_kv_cache_read_fp4(const void *kv_cache, const int64_t *slot_mapping, 
   if (!kv_cache || !slot_mapping || !k || !v) return PHOTON_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slot_mapping, 8))
     return PHOTON_ERR_INVALID_ARG;
-  Fp4ReadArgs a{kv_cache, slot_mapping, k, v, num_blocks * block_size, num_tokens, num_kv_heads, head_dim};
+  CacheReadArgs a{kv_cache, slot_mapping, k, v, num_blocks * block_size, num_tokens, num_kv_heads, head_dim};
   unsigned int *err = error_word();
   if (!err) return PHOTON_ERR_CUDA;
   return cuda_status(launch_kv_cache_read_fp4(a, out_dtype, err, reinterpret_cast<cudaStream_t>(stream)));
@@ -698,6 +702,200 @@ int photon_build_step_metadata_device(const int32_t *num_computed_tokens, const 
   unsigned int *err = error_word();
   if (!err) return PHOTON_ERR_CUDA;
   return cuda_status(launch_step_metadata(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- q/k norms in the write, 8-bit KV cache with a scale per block and head -----
+
+namespace photon {
+namespace {
+
+// Record pool of num_blocks blocks with 8-bit codes.
+int check_int8_pool(int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks) {
+  if (num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PHOTON_ERR_INVALID_ARG;
+  if (block_size != kBlockSize) return PHOTON_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PHOTON_ERR_UNSUPPORTED;
+  // 32-bit block ids; a grid has a warp for every KV head
+  if (num_blocks > INT32_MAX || num_kv_heads > 1024) return PHOTON_ERR_UNSUPPORTED;
+  return PHOTON_OK;
+}
+
+// What the writes with norms and the 8-bit writes check alike, and their
+// arguments.  *nothing: the call has no token and no query.
+int prepare_norm_write(void *q, const int32_t *q_positions, int32_t num_q_tokens, int32_t num_q_heads,
+                       const void *k, const void *v, const int32_t *positions, const int64_t *slot_mapping,
+                       const void *q_weight, const void *k_weight, bool norm, float eps, int32_t num_tokens,
+                       int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, photon_dtype dtype,
+                       float rope_theta, photon_rope rope_style, NormRopeArgs *a, bool *nothing) {
+  if (num_tokens < 0 || num_q_tokens < 0) return PHOTON_ERR_INVALID_ARG;
+  if (dtype != PHOTON_F32 && dtype != PHOTON_BF16) return PHOTON_ERR_INVALID_ARG;
+  if (rope_style != PHOTON_ROPE_NEOX && rope_style != PHOTON_ROPE_GPTJ && rope_style != PHOTON_ROPE_NONE)
+    return PHOTON_ERR_INVALID_ARG;
+  const bool rotate = rope_style != PHOTON_ROPE_NONE;
+  if (rotate && !(std::isfinite(rope_theta) && rope_theta > 0.f)) return PHOTON_ERR_INVALID_ARG;
+  if (norm && !(std::isfinite(eps) && eps > 0.f)) return PHOTON_ERR_INVALID_ARG;
+  if (num_q_tokens > 0) {
+    if (num_q_heads <= 0 || !q || !q_positions || !q_weight) return PHOTON_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(q_weight, 16) || !aligned(q_positions, 4)) return PHOTON_ERR_INVALID_ARG;
+    if (num_q_heads > kNormMaxHeads) return PHOTON_ERR_UNSUPPORTED;
+  }
+  if (num_tokens > 0) {
+    if (!k || !v || !positions || !slot_mapping || (norm && !k_weight)) return PHOTON_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
+        (norm && !aligned(k_weight, 16)))
+      return PHOTON_ERR_INVALID_ARG;
+  }
+  *nothing = num_tokens == 0 && num_q_tokens == 0;
+  a->q = q;
+  a->q_positions = q_positions;
+  a->q_weight = q_weight;
+  a->k = k;
+  a->v = v;
+  a->positions = positions;
+  a->slot_mapping = slot_mapping;
+  a->k_weight = k_weight;
+  a->num_slots = num_blocks * kBlockSize;
+  a->num_q_tokens = num_q_tokens;
+  a->num_q_heads = num_q_heads;
+  a->num_tokens = num_tokens;
+  a->num_kv_heads = num_kv_heads;
+  a->rope_style = rope_style;
+  a->eps = eps;
+  a->q_div = num_q_heads > 0 ? ((1u << 28) + num_q_heads - 1) / num_q_heads : 0;
+  a->kv_div = ((1u << 28) + num_kv_heads - 1) / num_kv_heads;
+  if (rotate && !*nothing) {
+    double freq[kMaxRopePairs];
+    frequencies(rope_theta, head_dim, freq);
+    for (int i = 0; i < head_dim / 2; ++i) {
+      const double x = freq[i] * 0.15915494309189533577;  // 1 / 2 pi: turns per position
+      a->turns[i] = static_cast<unsigned long long>((x - std::floor(x)) * 0x1p64);
+    }
+  }
+  return PHOTON_OK;
+}
+
+int write_int8_impl(void *q, const int32_t *q_positions, int32_t num_q_tokens, int32_t num_q_heads,
+                    const void *k, const void *v, const int32_t *positions, const int64_t *slot_mapping,
+                    const void *q_weight, const void *k_weight, bool norm, float eps, void *kv_cache,
+                    int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                    int64_t num_blocks, photon_dtype in_dtype, float rope_theta, photon_rope rope_style,
+                    photon_stream_t stream) {
+  int rc = check_int8_pool(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PHOTON_OK) return rc;
+  NormRopeArgs a{};
+  bool nothing = false;
+  rc = prepare_norm_write(q, q_positions, num_q_tokens, num_q_heads, k, v, positions, slot_mapping, q_weight,
+                          k_weight, norm, eps, num_tokens, num_kv_heads, head_dim, num_blocks, in_dtype, rope_theta,
+                          rope_style, &a, &nothing);
+  if (rc != PHOTON_OK || nothing) return rc;
+  if (num_tokens > 0 && (!kv_cache || !aligned(kv_cache, 16))) return PHOTON_ERR_INVALID_ARG;
+  a.k_cache = kv_cache;
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  return cuda_status(launch_kv_cache_write_int8(a, norm, in_dtype, head_dim, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+}  // namespace photon
+
+extern "C" {
+
+int photon_qk_norm_rope_kv_cache_write(void *q, const int32_t *q_positions, int32_t num_q_tokens,
+                                       int32_t num_q_heads, const void *k, const void *v,
+                                       const int32_t *positions, const int64_t *slot_mapping,
+                                       const void *q_weight, const void *k_weight, float eps, void *k_cache,
+                                       void *v_cache, int32_t num_tokens, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                       photon_dtype kv_dtype, float rope_theta, photon_rope rope_style,
+                                       photon_stream_t stream) {
+  if (num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PHOTON_ERR_INVALID_ARG;
+  if (block_size != kBlockSize) return PHOTON_ERR_UNSUPPORTED;
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256) return PHOTON_ERR_UNSUPPORTED;
+  if (num_kv_heads > kNormMaxHeads) return PHOTON_ERR_UNSUPPORTED;
+  if (num_blocks > INT64_MAX / (static_cast<int64_t>(num_kv_heads) * block_size * head_dim))
+    return PHOTON_ERR_INVALID_ARG;
+  photon::NormRopeArgs a{};
+  bool nothing = false;
+  const int rc = photon::prepare_norm_write(q, q_positions, num_q_tokens, num_q_heads, k, v, positions, slot_mapping,
+                                            q_weight, k_weight, true, eps, num_tokens, num_kv_heads, head_dim,
+                                            num_blocks, kv_dtype, rope_theta, rope_style, &a, &nothing);
+  if (rc != PHOTON_OK || nothing) return rc;
+  if (num_tokens > 0 && (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)))
+    return PHOTON_ERR_INVALID_ARG;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  return cuda_status(launch_qk_norm_rope_write(a, kv_dtype, head_dim, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t photon_kv_cache_int8_record_bytes(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? static_cast<size_t>(32 * head_dim + 16) : 0;
+}
+
+int photon_kv_cache_write_int8(const void *k, const void *v, const int32_t *positions,
+                               const int64_t *slot_mapping, void *kv_cache, int32_t num_tokens,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                               int64_t num_blocks, photon_dtype in_dtype, float rope_theta,
+                               photon_rope rope_style, photon_stream_t stream) {
+  return photon::write_int8_impl(nullptr, nullptr, 0, 0, k, v, positions, slot_mapping, nullptr, nullptr, false, 1.f,
+                                 kv_cache, num_tokens, num_kv_heads, head_dim, block_size, num_blocks, in_dtype,
+                                 rope_theta, rope_style, stream);
+}
+
+int photon_qk_norm_rope_kv_cache_write_int8(void *q, const int32_t *q_positions, int32_t num_q_tokens,
+                                            int32_t num_q_heads, const void *k, const void *v,
+                                            const int32_t *positions, const int64_t *slot_mapping,
+                                            const void *q_weight, const void *k_weight, float eps,
+                                            void *kv_cache, int32_t num_tokens, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                            photon_dtype in_dtype, float rope_theta, photon_rope rope_style,
+                                            photon_stream_t stream) {
+  return photon::write_int8_impl(q, q_positions, num_q_tokens, num_q_heads, k, v, positions, slot_mapping, q_weight,
+                                 k_weight, true, eps, kv_cache, num_tokens, num_kv_heads, head_dim, block_size,
+                                 num_blocks, in_dtype, rope_theta, rope_style, stream);
+}
+
+int photon_kv_cache_read_int8(const void *kv_cache, const int64_t *slot_mapping, void *k, void *v,
+                              int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int64_t num_blocks, photon_dtype out_dtype,
+                              photon_stream_t stream) {
+  if (num_tokens < 0) return PHOTON_ERR_INVALID_ARG;
+  if (out_dtype != PHOTON_F32 && out_dtype != PHOTON_BF16) return PHOTON_ERR_INVALID_ARG;
+  const int rc = photon::check_int8_pool(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PHOTON_OK || num_tokens == 0) return rc;
+  if (!kv_cache || !slot_mapping || !k || !v) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slot_mapping, 8))
+    return PHOTON_ERR_INVALID_ARG;
+  CacheReadArgs a{kv_cache, slot_mapping, k, v, num_blocks * block_size, num_tokens, num_kv_heads, head_dim};
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  return cuda_status(launch_kv_cache_read_int8(a, out_dtype, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int photon_paged_attention_decode_int8(const void *q, const void *kv_cache, const int32_t *block_tables,
+                                       const int32_t *context_lens, float scale, void *out,
+                                       int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                       int32_t max_blocks_per_seq, int32_t max_context_len,
+                                       int32_t partition_size, photon_dtype out_dtype, void *workspace,
+                                       size_t workspace_bytes, photon_stream_t stream) {
+  Prepared p{};
+  int rc = prepare_decode(q, kv_cache, kv_cache, block_tables, context_lens, scale, out, num_seqs,
+                          num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                          max_blocks_per_seq, max_context_len, partition_size, PHOTON_BF16,
+                          out_dtype, workspace, workspace_bytes, &p);
+  if (rc != PHOTON_OK) return rc;
+  rc = photon::check_int8_pool(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PHOTON_OK || num_seqs == 0) return rc;
+  if (max_context_len > INT32_MAX - 1024) return PHOTON_ERR_UNSUPPORTED;  // a step's tokens past the end stay int32
+  unsigned int *err = error_word();
+  if (!err) return PHOTON_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = cuda_status(launch_decode_partial_int8(p.args, err, st));
+  if (rc != PHOTON_OK || p.ws.total == 0) return rc;
+  return cuda_status(launch_decode_merge_fp4(p.args, st));
 }
 
 }  // extern "C"
