@@ -456,10 +456,55 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
   }
 }
 
-template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT>
-cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
+// Ring depth: about 100 to 130 KB of pages on their way per SM.  That is already
+// twice what the latency needs at the memory's rate, and what lies beyond it only
+// queues, unevenly: the warps served last at the start finish last.  Shallower
+// rings against deeper ones (128 contexts of up to 32k, d 64: three stages of two
+// pages in 16 warps 354 us, two stages 335; 64 ragged sequences of d 128: two
+// stages of two pages in 12 warps 48.4 us, in 8 warps 46.8).
+//
+// d 64, long steps: one CTA of 12 warps per SM instead of four of 4 (the warp
+// scheduler shares an SM evenly between a CTA's warps but prefers older CTAs): 335
+// -> 318 us on those 128 contexts, 0.99 of the copy rate.  Chosen when the page
+// bound -- sequences x ceil(max context / 16) x KV heads -- reaches
+// kLongPagesPerWarp per warp: 32 contexts of up to 8k (72) are even at 29.5 us, 16 of
+// up to 2048 (9) lose 4 %, one of 1024 12 %.  d 128 takes one CTA of 8 warps always.
+constexpr int64_t kLongPagesPerWarp = 64;
+
+inline int64_t page_bound(const DecodeArgs &a) {
+  return static_cast<int64_t>(a.num_seqs) * ((static_cast<int64_t>(a.ctx_cap) + kBlockSize - 1) / kBlockSize) *
+         a.num_kv_heads;
+}
+
+// When items are few and long, a CTA of four warps takes each: the piece count
+// of a row is bounded by the partition size (the workspace has no more slots), so
+// an idle GPU does not shorten them.  Teams are used where the least piece, or an
+// item without a workspace, has
+//  * 8 pages, without a workspace 4, and all items fit the GPU as CTAs at once (one
+//    context of 1024 in pieces of 8 pages, d 64 6.6 -> 5.1 us, d 128 9.2 -> 6.0;
+//    of 2 pages 4.9 -> 5.4, d 128 6.0 -> 6.4);
+//  * 16 pages, with more items: pieces as long as the workspace allows must leave
+//    warps idle (16 contexts of 2048 in partitions of 512, d 64 22.7 -> 11.1 us, d 128
+//    25.4 -> 19.1; 60 ragged ones of up to 1000 21.8 -> 16.6 and 32.7 -> 23.6; against
+//    it 16 of 2048 in partitions of 256 14.4 -> 15.2 and 17.3 -> 19.1), items without a
+//    workspace at most two to a CTA.  With 8 pages 16 of 2048 lose: 11.3 -> 15.2.
+constexpr int kTeamPages = 8, kTeamItemPages = 4, kTeamManyPages = 16;
+
+template <bool BAL>
+inline bool team_step(const DecodeArgs &a, int64_t items, int64_t ctas, int warps_per_cta) {
+  const int longest = (a.partition_size < a.ctx_cap ? a.partition_size : a.ctx_cap) / kBlockSize;
+  if (items <= ctas) return longest >= (BAL ? kTeamPages : kTeamItemPages);
+  if (longest < kTeamManyPages || a.num_kv_heads > ctas / 4) return false;
+  return BAL ? page_bound(a) <= ctas * warps_per_cta * (a.partition_size / kBlockSize) : items <= 2 * ctas;
+}
+
+enum class Int8Fit { kAlways, kLongSteps, kTeams };  // when launch_int8_kern takes a step
+
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, Int8Fit FIT>
+cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
+  constexpr bool TEAM = FIT == Int8Fit::kTeams;
   constexpr int SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
-  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, false>;
+  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, TEAM>;
   static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -475,27 +520,46 @@ cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_
     occupancy[dev].store(occ, std::memory_order_relaxed);
   }
   const int64_t items = static_cast<int64_t>(a.num_seqs) * a.max_partitions * a.num_kv_heads;
-  if (items == 0) return cudaSuccess;
-  const int64_t workers = std::min(items, static_cast<int64_t>(device_sm_count()) * occ * NW);
+  const int64_t ctas_cap = static_cast<int64_t>(device_sm_count()) * occ;
+  const int64_t warps_cap = ctas_cap * NW;
+  *taken = FIT == Int8Fit::kAlways ||
+           (FIT == Int8Fit::kTeams && team_step<BAL>(a, items, ctas_cap, NW)) ||
+           (FIT == Int8Fit::kLongSteps && items >= warps_cap && page_bound(a) >= kLongPagesPerWarp * warps_cap);
+  if (!*taken || items == 0) return cudaSuccess;
+  const int64_t workers = std::min(items, TEAM ? ctas_cap : warps_cap);
+  const int64_t grid = TEAM ? workers : (workers + NW - 1) / NW;
   DecodeArgs la = a;
   la.balanced = BAL ? 1 : 0;
-  return launch_pdl(kern, dim3(static_cast<unsigned>((workers + NW - 1) / NW)), dim3(NW * 32), SMEM, stream, la, err);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(NW * 32), SMEM, stream, la, err);
 }
 
-template <int D, int PP, int ST, int MIN_CTAS>
-cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
-  if (balanced_pieces(a))
-    return a.out_bf16 ? launch_int8_kern<D, PP, ST, 4, MIN_CTAS, true, false>(a, err, st)
-                      : launch_int8_kern<D, PP, ST, 4, MIN_CTAS, true, true>(a, err, st);
-  return a.out_bf16 ? launch_int8_kern<D, PP, ST, 4, MIN_CTAS, false, false>(a, err, st)
-                    : launch_int8_kern<D, PP, ST, 4, MIN_CTAS, false, true>(a, err, st);
+template <int D, bool BAL, bool SPLIT>
+cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
+  bool taken = false;
+  cudaError_t e = launch_int8_kern<D, 2, 2, 4, 1, BAL, SPLIT, Int8Fit::kTeams>(a, err, stream, &taken);
+  if (e != cudaSuccess || taken) return e;
+  if constexpr (D == 64) {
+    if constexpr (BAL) {
+      e = launch_int8_kern<D, 2, 2, 12, 1, true, SPLIT, Int8Fit::kLongSteps>(a, err, stream, &taken);
+      if (e != cudaSuccess || taken) return e;
+    }
+    return launch_int8_kern<D, 2, 2, 4, 4, BAL, SPLIT, Int8Fit::kAlways>(a, err, stream, &taken);
+  } else {
+    return launch_int8_kern<D, 2, 2, 8, 1, BAL, SPLIT, Int8Fit::kAlways>(a, err, stream, &taken);
+  }
+}
+
+template <int D>
+cudaError_t dispatch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
+  if (balanced_pieces(a)) return a.out_bf16 ? launch_int8<D, true, false>(a, err, st) : launch_int8<D, true, true>(a, err, st);
+  return a.out_bf16 ? launch_int8<D, false, false>(a, err, st) : launch_int8<D, false, true>(a, err, st);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
-  if (a.head_dim == 64) return launch_int8<64, 2, 3, 4>(a, err, st);
-  if (a.head_dim == 128) return launch_int8<128, 1, 3, 3>(a, err, st);
+  if (a.head_dim == 64) return dispatch_int8<64>(a, err, st);
+  if (a.head_dim == 128) return dispatch_int8<128>(a, err, st);
   return cudaErrorInvalidValue;
 }
 
