@@ -22,7 +22,6 @@
 // reduction for m, then the codes, 8 bytes per store.  A CTA takes the runs that
 // begin in its tile of tokens, all heads, over one (cos, sin) table.
 #include <climits>
-#include <cmath>
 
 #include "int8.cuh"
 #include "norm_rope.cuh"
@@ -37,14 +36,16 @@ static_assert(32 * kInt8Warps == kNormThreads, "query tiles run in the same CTAs
 
 constexpr float kCodeMagic = 12582912.f + 128.f;  // fma(y, r, this): low byte = rne(y r) + 128
 
-// Eight codes + 128, value i in byte i.
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float r) {
-  uint32_t b[8];
+// Codes + 128 of eight values, value i in byte i.
+__device__ __forceinline__ uint2 codes8(const float2 (&y)[4], float r) {
+  const float2 rr = make_float2(r, r), magic = make_float2(kCodeMagic, kCodeMagic);
+  uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(__fmaf_rn(y[i], r, kCodeMagic));
-  const uint32_t lo = __byte_perm(b[0], b[1], 0x0040u), hi = __byte_perm(b[2], b[3], 0x0040u);
-  const uint32_t lo2 = __byte_perm(b[4], b[5], 0x0040u), hi2 = __byte_perm(b[6], b[7], 0x0040u);
-  return make_uint2(__byte_perm(lo, hi, 0x5410u), __byte_perm(lo2, hi2, 0x5410u));
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __ffma2_rn(y[i], rr, magic);
+    b[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x0040u);
+  }
+  return make_uint2(__byte_perm(b[0], b[1], 0x5410u), __byte_perm(b[2], b[3], 0x5410u));
 }
 
 // Eight stored bytes as codes (exact).
@@ -63,141 +64,398 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   return r;
 }
 
-// One warp: K (which 0) or V (1) of one head of one run.  src: this lane's token
-// of row lane (0 .. 15) as an index into the tile's tokens, -1: not written.
-template <typename Tag, int D, bool NORM>
-__device__ __forceinline__ void write_run(const NormRopeArgs &a, int t0, int src, uint32_t written, int64_t block,
-                                          int h, int which, const float2 (*cs)[RopeRow<D>::STRIDE]) {
-  using T = typename Tag::T;
-  using R = RopeRow<D>;
-  constexpr int RPP = 32 / R::LPR, PASSES = kBlockSize / RPP;  // rows of a pass
-  const int lane = threadIdx.x & 31, w = lane % R::LPR, sub = lane / R::LPR;
-  const int H = a.num_kv_heads;
-  unsigned char *rec = static_cast<unsigned char *>(a.k_cache) + (block * H + h) * int8_record_bytes(D);
-  const T *x = static_cast<const T *>(which ? a.v : a.k) + static_cast<int64_t>(h) * D + 8 * w;
-  float *scale_at = reinterpret_cast<float *>(rec + int8_scale_byte(D, which));
-  const bool anew = written & 1u;
-  const float old = anew ? 0.f : *scale_at;
-  RowLoad<T> raw[PASSES];
-  int row_src[PASSES];
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    row_src[p] = __shfl_sync(0xffffffffu, src, p * RPP + sub);
-#pragma unroll
-    for (int i = 0; i < RowLoad<T>::N; ++i) raw[p].lo[i] = raw[p].hi[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (row_src[p] >= 0) raw[p].load(x + static_cast<int64_t>(t0 + row_src[p]) * H * D, R::HALF);
-  }
-  float y0[PASSES][8], y1[PASSES][8], m = 0.f;
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    RowLoad<T>::widen(raw[p].lo, y0[p]);
-    RowLoad<T>::widen(raw[p].hi, y1[p]);
-    if (!(written >> (p * RPP) & ((1u << RPP) - 1))) continue;  // no row of the pass is written: zeros
-    if (!which) {
-      if constexpr (NORM) {
-        float w0[8], w1[8];
-        load_weights<T>(a.k_weight, w, R::HALF, w0, w1);
-        rms_norm_lane<D>(y0[p], y1[p], w0, w1, a.eps);
-      }
-      if (a.rope_style != PHOTON_ROPE_NONE) {
-        const float2 *row = cs[max(row_src[p], 0)] + w;
-        if (a.rope_style == PHOTON_ROPE_GPTJ)
-          rotate_pairs<true>(y0[p], y1[p], row, R::LPR);
-        else
-          rotate_pairs<false>(y0[p], y1[p], row, R::LPR);
-      }
-    }
-    if (row_src[p] >= 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_abs3(m, y0[p][i], y1[p][i]);
-    }
-  }
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // a NaN's bits are the largest
-  float want = __fdiv_rn(m, 127.f);
-  if (want < kInt8Least) want = 0.f;
-  const bool finite = m <= 3.4028234663852886e38f;
-  const bool grows = finite && want > old;
-  const float scale = !finite ? __uint_as_float(0x7fffffffu) : grows ? fmaxf(want, 2.f * old) : old;
-  const float r = scale > 0.f ? __frcp_rn(scale) : 0.f;
-  const float ratio = __fmul_rn(old, r);
-  if (lane == 0) *scale_at = scale;
-  const bool requant = grows && !anew && old > 0.f;
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const uint32_t in_pass = written >> (p * RPP) & ((1u << RPP) - 1);
-    if (!in_pass && !anew && !requant) continue;
-    const int row = p * RPP + sub;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int e = 8 * w + half * R::HALF;
-      uint2 *at = reinterpret_cast<uint2 *>(rec + (which ? int8_v_byte(D, row, e) : int8_k_byte(row, e)));
-      if (row_src[p] >= 0) {
-        *at = scale > 0.f ? codes8(half ? y1[p] : y0[p], r) : make_uint2(0x80808080u, 0x80808080u);
-      } else if (anew) {
-        *at = make_uint2(0x80808080u, 0x80808080u);
-      } else if (requant) {
-        float c[8];
-        codes_to_f32(*at, c);
-        *at = codes8(c, ratio);
-      }
-    }
-  }
+// A run of several tokens as a warp sees it: lane o (0 .. 15) holds the token of row
+// o, as an index into the tile's tokens (-1: not written).
+struct Run {
+  int block;
+  uint32_t written;  // a bit per row
+  int src, any;      // any: the first token
+};
+
+// fl(m / 127) in fp32's normal range: a product, its exact residual, one
+// correction (equal to the division for every mantissa; tests/test_int8_host.py).
+__device__ __forceinline__ float div127(float m) {
+  constexpr float kInv = 1.f / 127.f;
+  const float q = __fmul_rn(m, kInv);
+  return __fmaf_rn(__fmaf_rn(-127.f, q, m), kInv, q);
 }
 
+// A row's scale after a write whose largest magnitude is m, and what follows from it.
+struct Scale {
+  float value, inv, ratio;  // ratio: for the codes of kept rows, where `grows`
+  bool some, grows;
+};
+__device__ __forceinline__ Scale new_scale(float m, float old) {
+  Scale s;
+  const float quo = div127(m), want = quo < kInt8Least ? 0.f : quo;
+  const bool finite = m <= 3.4028234663852886e38f;
+  s.grows = finite && want > old;
+  s.value = !finite ? __uint_as_float(0x7fffffffu) : s.grows ? fmaxf(want, 2.f * old) : old;
+  s.some = s.value > 0.f;
+  s.inv = s.some ? __frcp_rn(s.value) : 0.f;
+  s.ratio = __fmul_rn(old, s.inv);
+  s.grows = s.grows && old > 0.f;
+  return s;
+}
+
+__device__ __forceinline__ float max_abs_row(const LaneRow &y) {
+  float m = max_abs3(y.a[0].x, y.a[0].y, y.b[0].x);
+  m = max_abs3(m, y.b[0].y, y.a[1].x);
+  m = max_abs3(m, y.a[1].y, y.b[1].x);
+  m = max_abs3(m, y.b[1].y, y.a[2].x);
+  m = max_abs3(m, y.a[2].y, y.b[2].x);
+  m = max_abs3(m, y.b[2].y, y.a[3].x);
+  m = max_abs3(m, y.a[3].y, y.b[3].x);
+  return max_abs3(m, y.b[3].y, 0.f);
+}
+
+constexpr uint2 kZeroCodes = {0x80808080u, 0x80808080u};
+
 template <typename Tag, int D, bool NORM>
-__global__ void __launch_bounds__(kNormThreads)
-    kv_cache_write_int8_kernel(const __grid_constant__ NormRopeArgs a, unsigned int *err) {
+struct Write8 {
+  using T = typename Tag::T;
   using R = RopeRow<D>;
-  __shared__ float2 cs[kInt8TableRows][R::STRIDE];
+  static constexpr int RPP = 32 / R::LPR, PASSES = kBlockSize / RPP;  // rows of a pass
+  static_assert(RPP == 8 || RPP == 4, "head_dim 64 or 128");
+
+  __device__ __forceinline__ static unsigned char *record(const NormRopeArgs &a, int block, int h) {
+    return static_cast<unsigned char *>(a.k_cache) +
+           (static_cast<int64_t>(block) * a.num_kv_heads + h) * int8_record_bytes(D);
+  }
+  template <int WHICH>
+  __device__ __forceinline__ static int byte_of(int row, int e) {
+    return WHICH ? int8_v_byte(D, row, e) : int8_k_byte(row, e);
+  }
+
+  // Norm (NORM) and rotation of a K row, V as it is.
+  template <int WHICH>
+  __device__ __forceinline__ static void prepare(const NormRopeArgs &a, LaneRow &y, const RowLoad<T> &weight, int w,
+                                                 const float *row) {
+    if constexpr (!WHICH) {
+      const bool gptj = a.rope_style == PHOTON_ROPE_GPTJ;
+      if (a.rope_style == PHOTON_ROPE_NONE) row = nullptr;
+      if constexpr (NORM) {
+        LaneRow f;
+        widen_row(weight, f);
+        norm_rope_row<D>(y, f, a.eps, row, w, gptj);
+      } else if (row) {
+        rotate_row<D>(y, row, w, gptj);
+      }
+    }
+  }
+
+  // A lane's 16 codes of a row that the call does not write.
+  template <int WHICH>
+  __device__ __forceinline__ static void keep_row(unsigned char *rec, int row, int w, bool anew, float ratio) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint2 *at = reinterpret_cast<uint2 *>(rec + byte_of<WHICH>(row, 8 * w + half * R::HALF));
+      if (anew) {
+        *at = kZeroCodes;
+      } else {
+        float c[8];
+        codes_to_f32(*at, c);
+        const float2 f[4] = {make_float2(c[0], c[1]), make_float2(c[2], c[3]), make_float2(c[4], c[5]),
+                             make_float2(c[6], c[7])};
+        *at = codes8(f, ratio);
+      }
+    }
+  }
+
+  // ---- a run of several tokens: K (V: WHICH 1) of one head is a warp's unit of
+  // work, 16 rows by offset.  A lane holds 16 dims of one row per pass, rows 0, 1, 4,
+  // 5, 2, 3, 6, 7 and those + 8 in the order of the warp's row groups, so that the V
+  // bytes of half a warp fill whole 32-byte sectors; everything but a lane's first
+  // addresses is a constant.  All rows stay in registers, in fp32, from the scale to
+  // the codes: taking them twice from shared memory, with the registers of 24 warps
+  // per SM instead of 16, measured 16.1 -> 19.7 us (16384 tokens, 8 heads of 64).
+
+  // Row of pass p: that of pass 0 and this.
+  __device__ __forceinline__ static constexpr int row_step(int p) { return RPP == 8 ? 8 * p : 2 * (p & 1) + 8 * (p >> 1); }
+  __device__ __forceinline__ static int first_row(int lane) {
+    const int i = lane / R::LPR;
+    return (i & 1) | ((i >> 1) & 2) | ((i << 1) & 4);
+  }
+  __device__ __forceinline__ static constexpr uint32_t rows(int p) {
+    return RPP == 8 ? 0xffu << (8 * p) : 0x33u << row_step(p);
+  }
+  // Bytes of pass p and half `half` of the dims past those of pass 0, dims 8w.
+  template <int WHICH>
+  __device__ __forceinline__ static constexpr int byte_step(int p, int half) {
+    return WHICH ? 32 * (row_step(p) >> 3) + 512 * (row_step(p) >> 1 & 1) + half * (D == 64 ? 256 : 1024)
+                 : 256 * (row_step(p) >> 3) + 512 * (row_step(p) >> 1 & 1) + half * (D == 64 ? 32 : 1024);
+  }
+
+  struct Unit {
+    RowLoad<T> raw[PASSES];
+    float old;  // the block's scale so far
+  };
+
+  // Starts unit u's loads (K of head u / 2, V where u is odd).  Rows that are not
+  // written take the run's first token: their values go nowhere.
+  __device__ __forceinline__ static void load(Unit &unit, const NormRopeArgs &a, const Run &run, int t0, int u,
+                                              int lane) {
+    const T *x = static_cast<const T *>(u & 1 ? a.v : a.k) +
+                 (static_cast<int64_t>(t0) * a.num_kv_heads + (u >> 1)) * D + 8 * (lane % R::LPR);
+    const int token = a.num_kv_heads * D;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!(run.written & rows(p))) continue;
+      const int src = __shfl_sync(0xffffffffu, run.src, first_row(lane) + row_step(p));
+      unit.raw[p].load(x + static_cast<int64_t>(src < 0 ? run.any : src) * token, R::HALF);
+    }
+    unit.old = run.written & 1u
+                   ? 0.f
+                   : *reinterpret_cast<const float *>(record(a, run.block, u >> 1) + int8_scale_byte(D, u & 1));
+  }
+
+  template <int WHICH>
+  __device__ __forceinline__ static void write(const NormRopeArgs &a, const Run &run, int h, int lane,
+                                               LaneRow (&y)[PASSES], float old, const float (*cs)[R::STRIDE]) {
+    const int w = lane % R::LPR, row0 = first_row(lane);
+    const bool anew = run.written & 1u;
+    float m = 0.f;
+    RowLoad<T> weight;
+    if (NORM && !WHICH) weight.load(static_cast<const T *>(a.k_weight) + 8 * w, R::HALF);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!(run.written & rows(p))) continue;
+      const int src = WHICH ? 0 : __shfl_sync(0xffffffffu, run.src, row0 + row_step(p));
+      prepare<WHICH>(a, y[p], weight, w, cs[src < 0 ? run.any : src]);
+      const float top = max_abs_row(y[p]);
+      if (run.written >> (row0 + row_step(p)) & 1u) m = max_abs3(m, top, 0.f);
+    }
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // a NaN's bits are the largest
+    const Scale s = new_scale(m, old);
+    unsigned char *rec = record(a, run.block, h);
+    if (lane == 0) *reinterpret_cast<float *>(rec + int8_scale_byte(D, WHICH)) = s.value;
+    unsigned char *at = rec + byte_of<WHICH>(row0, 8 * w);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!(run.written & rows(p))) continue;
+      const uint2 lo = s.some ? codes8(y[p].a, s.inv) : kZeroCodes, hi = s.some ? codes8(y[p].b, s.inv) : kZeroCodes;
+      if (run.written >> (row0 + row_step(p)) & 1u) {
+        *reinterpret_cast<uint2 *>(at + byte_step<WHICH>(p, 0)) = lo;
+        *reinterpret_cast<uint2 *>(at + byte_step<WHICH>(p, 1)) = hi;
+      }
+    }
+    if (run.written == 0xffffu || !(anew || s.grows)) return;
+#pragma unroll 1
+    for (int row = lane / R::LPR; row < kBlockSize; row += RPP)
+      if (!(run.written >> row & 1u)) keep_row<WHICH>(rec, row, w, anew, s.ratio);
+  }
+
+  // ---- a run of one token: K or V of as many heads as the warp has row groups, one
+  // row each.  (As runs of several, 28 of 32 lanes would have no work: 2048 tokens
+  // of a decode step, 8 heads of 64, 17.0 us.)
+  struct Single {
+    RowLoad<T> raw;
+    float old;
+  };
+  __device__ __forceinline__ static int groups(const NormRopeArgs &a) { return (a.num_kv_heads + RPP - 1) / RPP; }
+
+  // token: its index in the call.  Heads past the last take the last one's row.
+  __device__ __forceinline__ static void load_single(Single &s, const NormRopeArgs &a, int64_t token, int block, int off,
+                                                     int u, int lane) {
+    const int h = min((u >> 1) * RPP + lane / R::LPR, a.num_kv_heads - 1);
+    s.raw.load(static_cast<const T *>(u & 1 ? a.v : a.k) + (token * a.num_kv_heads + h) * D + 8 * (lane % R::LPR),
+               R::HALF);
+    s.old = off == 0 ? 0.f : *reinterpret_cast<const float *>(record(a, block, h) + int8_scale_byte(D, u & 1));
+  }
+
+  template <int WHICH>
+  __device__ __forceinline__ static void write_single(const NormRopeArgs &a, const Single &in, int block, int off,
+                                                      int group, int lane, const float *row) {
+    const int w = lane % R::LPR, h = group * RPP + lane / R::LPR;
+    RowLoad<T> weight;
+    if (NORM && !WHICH) weight.load(static_cast<const T *>(a.k_weight) + 8 * w, R::HALF);
+    LaneRow y;
+    widen_row(in.raw, y);
+    prepare<WHICH>(a, y, weight, w, row);
+    float m = max_abs_row(y);
+#pragma unroll
+    for (int o = R::LPR / 2; o > 0; o >>= 1) m = max_abs3(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+    if (h < a.num_kv_heads) {
+      const Scale s = new_scale(m, in.old);
+      unsigned char *rec = record(a, block, h);
+      if (w == 0) *reinterpret_cast<float *>(rec + int8_scale_byte(D, WHICH)) = s.value;
+      unsigned char *at = rec + byte_of<WHICH>(off, 8 * w);
+      *reinterpret_cast<uint2 *>(at) = s.some ? codes8(y.a, s.inv) : kZeroCodes;
+      *reinterpret_cast<uint2 *>(at + byte_step<WHICH>(0, 1)) = s.some ? codes8(y.b, s.inv) : kZeroCodes;
+      if (off == 0 || s.grows)
+#pragma unroll 1
+        for (int i = 0; i < kBlockSize; ++i)
+          if (i != off) keep_row<WHICH>(rec, i, w, off == 0, s.ratio);
+    }
+    __syncwarp();
+  }
+};
+
+// CTAs per SM that the write's registers allow.
+template <typename T, int D>
+constexpr int int8_write_ctas() {
+  return D == 64 ? 2 : 1;
+}
+
+// The first kv_ctas CTAs walk the tiles of tokens, the others take a query tile
+// each.  A tile's slots and positions are loaded one tile ahead, a unit's rows and
+// scale one unit ahead, across runs and tiles.
+template <typename Tag, int D, bool NORM>
+__global__ void __launch_bounds__(kNormThreads, int8_write_ctas<typename Tag::T, D>())
+    kv_cache_write_int8_kernel(const __grid_constant__ NormRopeArgs a, int kv_ctas, int tiles, unsigned int *err) {
+  using R = RopeRow<D>;
+  using W = Write8<Tag, D, NORM>;
+  __shared__ __align__(16) float cs[2][kInt8TableRows][R::STRIDE];  // of this tile and the next
   pdl_wait();
   pdl_launch_dependents();
   if constexpr (NORM) {
-    if (static_cast<int>(blockIdx.x) < a.q_tiles) {
-      norm_rope_q_tile<Tag, D>(a, blockIdx.x, cs);
+    if (static_cast<int>(blockIdx.x) >= kv_ctas) {
+      norm_rope_q_tile<Tag, D>(a, blockIdx.x - kv_ctas, cs[0]);
       return;
     }
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = (blockIdx.x - (NORM ? a.q_tiles : 0)) << a.tile_log2, tile = 1 << a.tile_log2;
-  // lane i looks at token t0 - 1 + i: a run's length is at most a block's 16, so
-  // the runs that begin in a tile of 16 end within the warp's 32 tokens
-  const int t = t0 - 1 + lane;
-  int64_t slot = t >= 0 && t < a.num_tokens ? a.slot_mapping[t] : -1;
-  if (slot >= a.num_slots) {
-    if (warp == 0 && lane >= 1 && lane <= tile) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
-    slot = -1;
-  }
-  const bool live = slot >= 0;
-  const int64_t block = slot >> 4;
-  const int64_t before = __shfl_up_sync(0xffffffffu, block, 1);
-  const bool same = lane > 0 && live && before == block;
-  const uint32_t joined = __ballot_sync(0xffffffffu, same);
-  uint32_t leaders = __ballot_sync(0xffffffffu, lane >= 1 && lane <= tile && live && !same);
-  if (!leaders) return;  // the same in every warp
+  const int units = 2 * a.num_kv_heads;  // K and V of every head, over the warps
+  const bool rotate = a.rope_style != PHOTON_ROPE_NONE;
+  // The open tile: lane i looks at token t0 - 1 + i.  A run's length is at most a
+  // block's 16, so the runs that begin in a tile of 16 end within the 32 tokens.
+  // singles, leaders: where runs of one, of several tokens begin.
+  int tile = static_cast<int>(blockIdx.x) - kv_ctas, t0 = 0, block = 0, off = 0, pos = 0, first = 0, last = 0;
+  uint32_t joined = 0, rising = 0, leaders = 0, singles = 0;
+  int64_t slot1 = -1;  // of the next tile
+  int pos1 = 0;
+  auto fetch = [&](int k) {
+    const int64_t t = (static_cast<int64_t>(k) << a.tile_log2) - 1 + lane;
+    const bool in = k < tiles && t >= 0 && t < a.num_tokens;
+    slot1 = in ? a.slot_mapping[t] : -1;
+    pos1 = in && rotate ? a.positions[t] : 0;
+  };
   // tokens that follow lane i in its run
-  auto follow = [&](int i) { return i == 31 ? 0 : min(__ffs(~(joined >> (i + 1))) - 1, kBlockSize - 1); };
-  if (a.rope_style != PHOTON_ROPE_NONE) {
-    const int i0 = __ffs(leaders) - 1, i1 = 31 - __clz(leaders);
-    const int n = i1 + follow(i1) + 1 - i0;
-    rope_table_rows<D>(cs + (i0 - 1), a.positions + (t0 - 1 + i0), n, a.turns,
-                       a.rope_style == PHOTON_ROPE_GPTJ, kNormThreads);
-    __syncthreads();
-  }
-  const int H = a.num_kv_heads;
-  while (leaders) {  // a run: its heads' K and V over the warps
-    const int i = __ffs(leaders) - 1;
+  auto follow = [&](int i) { return min(__ffs(~(joined >> (i + 1))) - 1, kBlockSize - 1); };
+  Run run;
+  auto take_run = [&]() {
+    const int i = __ffs(leaders) - 1, n = follow(i);
     leaders &= leaders - 1;
-    const int len = 1 + follow(i);
-    const int64_t b = __shfl_sync(0xffffffffu, block, i);
-    int src = -1;  // row lane's token, the last of those with its slot
-    uint32_t written = 0;
-    for (int j = 0; j < len; ++j) {
-      const int off = static_cast<int>(__shfl_sync(0xffffffffu, slot, i + j)) & (kBlockSize - 1);
-      if (lane == off) src = i - 1 + j;
-      written |= 1u << off;
+    run.block = __shfl_sync(0xffffffffu, block, i);
+    run.any = i - 1;
+    const int o = __shfl_sync(0xffffffffu, off, i);
+    const uint32_t rest = ((1u << n) - 1) << (i + 1);
+    if ((rising & rest) == rest) {  // offsets in order: the rule
+      run.written = ((2u << n) - 1) << o;
+      run.src = lane >= o && lane <= o + n ? i - 1 + lane - o : -1;
+    } else {  // the last token of those with a row's slot
+      run.written = 0;
+      run.src = -1;
+      for (int j = 0; j <= n; ++j) {
+        const int at = __shfl_sync(0xffffffffu, off, i + j);
+        if (lane == at) run.src = i - 1 + j;
+        run.written |= 1u << at;
+      }
     }
-    for (int hv = warp; hv < 2 * H; hv += kInt8Warps)
-      write_run<Tag, D, NORM>(a, t0, src, written, b, hv >> 1, hv & 1, cs);
+  };
+  typename W::Unit unit{};
+  typename W::Single ahead{};
+  bool have = false;  // `unit` holds the warp's first unit of the open tile's runs of several tokens
+  auto load_single = [&](int j) {  // the warp's j-th unit of the runs of one token
+    const int n = 2 * W::groups(a);
+    uint32_t left = singles;
+    for (; j >= n; j -= n) left &= left - 1;
+    const int i = __ffs(left) - 1;
+    W::load_single(ahead, a, static_cast<int64_t>(t0) - 1 + i, __shfl_sync(0xffffffffu, block, i),
+                   __shfl_sync(0xffffffffu, off, i), j, lane);
+  };
+  // Opens the CTA's next tile in which a run begins, the same in every warp, and
+  // starts the warp's first loads there.
+  auto next_tile = [&]() -> bool {
+    for (tile += kv_ctas; tile < tiles; tile += kv_ctas) {
+      int64_t slot = slot1;
+      pos = pos1;
+      fetch(tile + kv_ctas);
+      t0 = tile << a.tile_log2;
+      const bool own = lane >= 1 && lane <= 1 << a.tile_log2;
+      if (slot >= a.num_slots) {
+        if (warp == 0 && own) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
+        slot = -1;
+      }
+      const bool live = slot >= 0;
+      block = live ? static_cast<int>(slot >> 4) : -1;
+      off = static_cast<int>(slot) & (kBlockSize - 1);
+      const int before = __shfl_up_sync(0xffffffffu, block, 1);
+      const bool same = lane > 0 && live && before == block;
+      joined = __ballot_sync(0xffffffffu, same);
+      const int off_before = __shfl_up_sync(0xffffffffu, off, 1);
+      rising = __ballot_sync(0xffffffffu, off_before + 1 == off);
+      leaders = __ballot_sync(0xffffffffu, own && live && !same);
+      if (!leaders) continue;
+      first = __ffs(leaders) - 1;  // the tile's runs cover lanes first .. last
+      last = 31 - __clz(leaders);
+      last += follow(last);
+      singles = leaders & ~(joined >> 1);
+      leaders &= ~singles;
+      have = leaders && warp < units;
+      if (have) {
+        take_run();
+        W::load(unit, a, run, t0, warp, lane);
+      } else if (warp < __popc(singles) * 2 * W::groups(a)) {
+        load_single(warp);
+      }
+      return true;
+    }
+    return false;
+  };
+  fetch(blockIdx.x);
+  if (!next_tile()) return;
+  for (int buf = 0;; buf ^= 1) {
+    if (rotate) {
+      rope_table_rows<D>(cs[buf] + (first - 1), pos, first, last + 1 - first, a.turns,
+                         a.rope_style == PHOTON_ROPE_GPTJ);
+      __syncthreads();  // the table of the tile before last is free: its readers passed the barrier since
+    }
+    const int n1 = 2 * W::groups(a);
+    for (int j = warp; j < __popc(singles) * n1; j += kInt8Warps) {
+      if (j != warp || have) load_single(j);
+      uint32_t left = singles;
+      int u = j;
+      for (; u >= n1; u -= n1) left &= left - 1;
+      const int i = __ffs(left) - 1;
+      const int b = __shfl_sync(0xffffffffu, block, i), o = __shfl_sync(0xffffffffu, off, i);
+      if (u & 1)
+        W::template write_single<1>(a, ahead, b, o, u >> 1, lane, cs[buf][i - 1]);
+      else
+        W::template write_single<0>(a, ahead, b, o, u >> 1, lane, cs[buf][i - 1]);
+    }
+    bool more = true;  // there is another tile
+    if (!have) {
+      more = next_tile();
+    } else {
+      for (int u = warp;;) {
+        LaneRow y[W::PASSES];
+#pragma unroll
+        for (int p = 0; p < W::PASSES; ++p) widen_row(unit.raw[p], y[p]);
+        const float old = unit.old;
+        const Run now = run;
+        const int u0 = u;
+        bool open = true;
+        u += kInt8Warps;
+        if (u >= units) {
+          u = warp;
+          if (leaders)
+            take_run();
+          else
+            open = false;
+        }
+        if (open)
+          W::load(unit, a, run, t0, u, lane);
+        else
+          more = next_tile();
+        if (u0 & 1)
+          W::template write<1>(a, now, u0 >> 1, lane, y, old, cs[buf]);
+        else
+          W::template write<0>(a, now, u0 >> 1, lane, y, old, cs[buf]);
+        if (!open) break;
+      }
+    }
+    if (!more) return;
   }
 }
 
@@ -271,26 +529,41 @@ cudaError_t launch_read(const CacheReadArgs &a, unsigned int *err, cudaStream_t 
 }
 
 template <typename Tag, int D>
-cudaError_t launch_write(const NormRopeArgs &a, bool norm, int64_t ctas, unsigned int *err, cudaStream_t st) {
+cudaError_t launch_write(NormRopeArgs a, bool norm, unsigned int *err, cudaStream_t st) {
+  const int64_t room0 = static_cast<int64_t>(device_sm_count()) * int8_write_ctas<typename Tag::T, D>();
+  a.tile_log2 = 0;
+  while ((1 << a.tile_log2) < kInt8MaxTile && (static_cast<int64_t>(a.num_tokens) >> a.tile_log2) > room0) ++a.tile_log2;
+  const int64_t tiles = (static_cast<int64_t>(a.num_tokens) + (1 << a.tile_log2) - 1) >> a.tile_log2;
+  const int64_t room = static_cast<int64_t>(device_sm_count()) * int8_write_ctas<typename Tag::T, D>();
+  const int64_t kv_ctas = tiles < room ? tiles : room, ctas = kv_ctas + a.q_tiles;
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > INT32_MAX || tiles + kv_ctas > INT32_MAX) return cudaErrorInvalidValue;
   auto kern = norm ? kv_cache_write_int8_kernel<Tag, D, true> : kv_cache_write_int8_kernel<Tag, D, false>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), 0, st, a, err);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), 0, st, a,
+                    static_cast<int>(kv_ctas), static_cast<int>(tiles), err);
 }
 
 }  // namespace
 
+// Query rows from which they get a launch of their own, in the bf16 / fp32 write's
+// kernel: this one's registers leave 8 or 16 warps per SM, that one's 32.  262144 rows of d
+// 128 with 16384 tokens: 90.9 -> 71.5 us; 131072 of d 64 with 4096 tokens 10.9 against 14.2.
+constexpr int64_t kQueryRowsApart = 262144;
+
 cudaError_t launch_kv_cache_write_int8(NormRopeArgs a, bool norm, photon_dtype in_dt, int head_dim,
                                        unsigned int *err, cudaStream_t st) {
+  if (static_cast<int64_t>(a.num_q_tokens) * a.num_q_heads >= kQueryRowsApart) {
+    NormRopeArgs q = a;
+    q.num_tokens = 0;
+    const cudaError_t e = launch_qk_norm_rope_write(q, in_dt, head_dim, err, st);
+    if (e != cudaSuccess) return e;
+    a.num_q_tokens = 0;
+  }
   a.q_tile_log2 = norm_tile_log2(a.num_q_tokens, 3);
-  a.tile_log2 = norm_tile_log2(a.num_tokens, 4);
   a.q_tiles = static_cast<int>((static_cast<int64_t>(a.num_q_tokens) + (1 << a.q_tile_log2) - 1) >> a.q_tile_log2);
-  const int64_t ctas = a.q_tiles + ((static_cast<int64_t>(a.num_tokens) + (1 << a.tile_log2) - 1) >> a.tile_log2);
-  if (ctas == 0) return cudaSuccess;
-  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   if (head_dim == 64)
-    return in_dt == PHOTON_BF16 ? launch_write<BF16Tag, 64>(a, norm, ctas, err, st)
-                                : launch_write<F32Tag, 64>(a, norm, ctas, err, st);
-  return in_dt == PHOTON_BF16 ? launch_write<BF16Tag, 128>(a, norm, ctas, err, st)
-                              : launch_write<F32Tag, 128>(a, norm, ctas, err, st);
+    return in_dt == PHOTON_BF16 ? launch_write<BF16Tag, 64>(a, norm, err, st) : launch_write<F32Tag, 64>(a, norm, err, st);
+  return in_dt == PHOTON_BF16 ? launch_write<BF16Tag, 128>(a, norm, err, st) : launch_write<F32Tag, 128>(a, norm, err, st);
 }
 
 cudaError_t launch_kv_cache_read_int8(const CacheReadArgs &a, photon_dtype out_dt, unsigned int *err,

@@ -24,17 +24,46 @@ constexpr int kNormThreads = 256;
 constexpr int kNormMaxTile = 8;    // tokens of a CTA
 constexpr int kNormDivBits = 28;   // row / heads = row * div >> 28
 
-// A token's (cos, sin) in the order its lanes read them: step i of lane w at
-// i * LPR + w.  Rows are padded by LPR entries: neighbouring rows of a table then
-// start in different banks, where a warp's lanes read several tokens at once.
+// A lane's 16 values of a row, as pairs of neighbouring dims for the packed fp32
+// instructions (two elements each): a: dims 8w .. 8w + 7, b: those + D/2.
+struct LaneRow {
+  float2 a[4], b[4];
+};
+
+template <typename T>
+__device__ __forceinline__ void widen_row(const RowLoad<T> &r, LaneRow &x) {
+  float f[8];
+  RowLoad<T>::widen(r.lo, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.a[j] = make_float2(f[2 * j], f[2 * j + 1]);
+  RowLoad<T>::widen(r.hi, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.b[j] = make_float2(f[2 * j], f[2 * j + 1]);
+}
+
+// To the storage type, one rounding each; dst: the lane's dims 8w.
+template <typename T>
+__device__ __forceinline__ void store_row(T *dst, int half, const LaneRow &x) {
+  const float lo[8] = {x.a[0].x, x.a[0].y, x.a[1].x, x.a[1].y, x.a[2].x, x.a[2].y, x.a[3].x, x.a[3].y};
+  const float hi[8] = {x.b[0].x, x.b[0].y, x.b[1].x, x.b[1].y, x.b[2].x, x.b[2].y, x.b[3].x, x.b[3].y};
+  store8(dst, lo);
+  store8(dst + half, hi);
+}
+
+// A token's rotations in the order its lanes read them: step j of lane w, two
+// pairs, is the chunk (cos, cos, sin, sin) at 4 (j LPR + w) floats.  At D = 64 rows
+// are padded so that two tokens read by one quarter of a warp meet no bank twice.
 template <int D>
 struct RopeRow {
   static constexpr int LPR = D / 16;  // lanes of a row
   static constexpr int HALF = D / 2;
-  static constexpr int STRIDE = HALF + LPR;
-  // step and lane of a pair: NEOX lane w takes pairs 8w .., GPT-J 4w .. of either half
+  static constexpr int STRIDE = 2 * HALF + (D == 64 ? 16 : 0);
+  // Where a pair's cosine lies (its sine 2 further).  NEOX lane w takes pairs
+  // 8w .. 8w + 7 in order; GPT-J 4w .. 4w + 3, then those + D/4.
   __device__ __forceinline__ static int at(int pair, bool gptj) {
-    return gptj ? (pair / (D / 4) * 4 + pair % 4) * LPR + pair % (D / 4) / 4 : pair % 8 * LPR + pair / 8;
+    const int p = pair % (D / 4);
+    const int lane = gptj ? p / 4 : pair / 8, i = gptj ? pair / (D / 4) * 4 + p % 4 : pair % 8;
+    return 4 * (i / 2 * LPR + lane) + i % 2;
   }
 };
 
@@ -52,65 +81,111 @@ __device__ __forceinline__ float2 cos_sin_of_turn(unsigned long long turn) {
 
 // Table rows 0 .. n - 1 of the positions pos[0 .. n - 1], by all threads of the CTA.
 template <int D>
-__device__ __forceinline__ void rope_table_rows(float2 (*cs)[RopeRow<D>::STRIDE], const int32_t *pos, int n,
-                                                const unsigned long long *turns, bool gptj, int threads) {
+__device__ __forceinline__ void rope_table_rows(float (*cs)[RopeRow<D>::STRIDE], const int32_t *pos, int n,
+                                                const unsigned long long *turns, bool gptj) {
   using R = RopeRow<D>;
-  for (int i = threadIdx.x; i < n * R::HALF; i += threads) {
+  for (int i = threadIdx.x; i < n * R::HALF; i += kNormThreads) {
     const int t = i / R::HALF, pair = i % R::HALF;
-    cs[t][R::at(pair, gptj)] =
+    const float2 v =
         cos_sin_of_turn(static_cast<unsigned long long>(static_cast<long long>(pos[t])) * turns[pair]);
+    float *at = cs[t] + R::at(pair, gptj);
+    at[0] = v.x;
+    at[2] = v.y;
   }
 }
 
-// Rotates a lane's 8 pairs.  NEOX: (x0[i], x1[i]); GPT-J: (x0[2i], x0[2i + 1]),
-// then those of x1.  cs: the lane's first entry of its token's table row.
-template <bool GPTJ>
-__device__ __forceinline__ void rotate_pairs(float (&x0)[8], float (&x1)[8], const float2 *cs, int stride) {
+// The same of positions that lie in a warp's lanes, pos of lane `lane0 + t` for row
+// t: with D >= 64 every 32 entries belong to one token.
+template <int D>
+__device__ __forceinline__ void rope_table_rows(float (*cs)[RopeRow<D>::STRIDE], int pos, int lane0, int n,
+                                                const unsigned long long *turns, bool gptj) {
+  using R = RopeRow<D>;
+  static_assert(R::HALF % 32 == 0, "a warp's entries are one token's");
+  for (int i = threadIdx.x; i < n * R::HALF; i += kNormThreads) {
+    const int t = i / R::HALF, pair = i % R::HALF;
+    const int p = __shfl_sync(0xffffffffu, pos, lane0 + t);
+    const float2 v = cos_sin_of_turn(static_cast<unsigned long long>(static_cast<long long>(p)) * turns[pair]);
+    float *at = cs[t] + R::at(pair, gptj);
+    at[0] = v.x;
+    at[2] = v.y;
+  }
+}
+
+// Rotates a lane's 8 pairs.  NEOX: (a, b) element by element; GPT-J: the
+// neighbours of a, then of b.  cs: the token's table row.
+template <int D>
+__device__ __forceinline__ void rotate_row(LaneRow &x, const float *cs, int w, bool gptj) {
+  using R = RopeRow<D>;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float &u = GPTJ ? (i < 4 ? x0[2 * i] : x1[2 * i - 8]) : x0[i];
-    float &w = GPTJ ? (i < 4 ? x0[2 * i + 1] : x1[2 * i - 7]) : x1[i];
-    const float2 p = cs[i * stride];
-    const float a = u, b = w;
-    u = fmaf(a, p.x, -(b * p.y));
-    w = fmaf(b, p.x, a * p.y);
+  for (int j = 0; j < 4; ++j) {
+    const float4 t = *reinterpret_cast<const float4 *>(cs + 4 * (j * R::LPR + w));
+    if (gptj) {
+      float2 &p = j < 2 ? x.a[2 * j] : x.b[2 * j - 4], &q = j < 2 ? x.a[2 * j + 1] : x.b[2 * j - 3];
+      p = make_float2(fmaf(p.x, t.x, -(p.y * t.z)), fmaf(p.y, t.x, p.x * t.z));
+      q = make_float2(fmaf(q.x, t.y, -(q.y * t.w)), fmaf(q.y, t.y, q.x * t.w));
+    } else {
+      const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), u = x.a[j], v = x.b[j];
+      x.a[j] = __ffma2_rn(u, c, __fmul2_rn(v, make_float2(-t.z, -t.w)));
+      x.b[j] = __ffma2_rn(v, c, __fmul2_rn(u, s));
+    }
   }
 }
 
 // The lane's weights of a norm, as fp32.
 template <typename T>
-__device__ __forceinline__ void load_weights(const void *weight, int w, int half, float (&w0)[8], float (&w1)[8]) {
+__device__ __forceinline__ void load_weights(const void *weight, int w, int half, LaneRow &out) {
   RowLoad<T> r;
   r.load(static_cast<const T *>(weight) + 8 * w, half);
-  RowLoad<T>::widen(r.lo, w0);
-  RowLoad<T>::widen(r.hi, w1);
+  widen_row(r, out);
 }
 
-// x * w / sqrt(mean square + eps) of a row of D values; all lanes of the warp take part.
-template <int D>
-__device__ __forceinline__ void rms_norm_lane(float (&x0)[8], float (&x1)[8], const float (&w0)[8],
-                                              const float (&w1)[8], float eps) {
-  float a = 0.f, b = 0.f;
+__device__ __forceinline__ void scale_row(LaneRow &x, const LaneRow &f) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a = fmaf(x0[i], x0[i], a);
-    b = fmaf(x1[i], x1[i], b);
+  for (int j = 0; j < 4; ++j) {
+    x.a[j] = __fmul2_rn(x.a[j], f.a[j]);
+    x.b[j] = __fmul2_rn(x.b[j], f.b[j]);
   }
-  a += b;
+}
+__device__ __forceinline__ void scale_row(LaneRow &x, float f) {
+  const float2 ff = make_float2(f, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x.a[j] = __fmul2_rn(x.a[j], ff);
+    x.b[j] = __fmul2_rn(x.b[j], ff);
+  }
+}
+
+// 1 / sqrt(mean square + eps) of a row of D values; all lanes of the warp take part.
+template <int D>
+__device__ __forceinline__ float inv_rms(const LaneRow &x, float eps) {
+  float2 s = __fmul2_rn(x.a[0], x.a[0]), t = __fmul2_rn(x.b[0], x.b[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) {
+    s = __ffma2_rn(x.a[j], x.a[j], s);
+    t = __ffma2_rn(x.b[j], x.b[j], t);
+  }
+  s = __fadd2_rn(s, t);
+  float a = s.x + s.y;
 #pragma unroll
   for (int o = RopeRow<D>::LPR / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  const float inv = rsqrtf(fmaf(a, 1.f / D, eps));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x0[i] *= inv * w0[i];
-    x1[i] *= inv * w1[i];
-  }
+  return rsqrtf(fmaf(a, 1.f / D, eps));
+}
+
+// Norm and rotation of a row: the sum's shuffles run beside the rotation of x w,
+// the factor comes last.  cs NULL: no rotation.
+template <int D>
+__device__ __forceinline__ void norm_rope_row(LaneRow &x, const LaneRow &weight, float eps, const float *cs, int w,
+                                              bool gptj) {
+  const float inv = inv_rms<D>(x, eps);
+  scale_row(x, weight);
+  if (cs) rotate_row<D>(x, cs, w, gptj);
+  scale_row(x, inv);
 }
 
 // One tile of query rows, [tokens][heads][D] contiguous: normalised and rotated
 // in place, neighbouring rows of a token by neighbouring lanes.
 template <typename Tag, int D>
-__device__ __forceinline__ void norm_rope_q_tile(const NormRopeArgs &a, int tile, float2 (*cs)[RopeRow<D>::STRIDE]) {
+__device__ __forceinline__ void norm_rope_q_tile(const NormRopeArgs &a, int tile, float (*cs)[RopeRow<D>::STRIDE]) {
   using T = typename Tag::T;
   using R = RopeRow<D>;
   constexpr int STEP = kNormThreads / R::LPR;
@@ -121,28 +196,18 @@ __device__ __forceinline__ void norm_rope_q_tile(const NormRopeArgs &a, int tile
   T *base = static_cast<T *>(a.q) + static_cast<int64_t>(t0) * a.num_q_heads * D + 8 * w;
   RowLoad<T> next;
   next.load(base + min(first, rows - 1) * D, R::HALF);
-  float w0[8], w1[8];
-  load_weights<T>(a.q_weight, w, R::HALF, w0, w1);
-  if (rotate) rope_table_rows<D>(cs, a.q_positions + t0, n, a.turns, gptj, kNormThreads);
+  LaneRow weight;
+  load_weights<T>(a.q_weight, w, R::HALF, weight);
+  if (rotate) rope_table_rows<D>(cs, a.q_positions + t0, n, a.turns, gptj);
   __syncthreads();
   for (int r0 = 0; r0 < rows; r0 += STEP) {  // lanes past the last row repeat it, for the shuffles
     const int r = min(r0 + first, rows - 1);
-    float x0[8], x1[8];
-    RowLoad<T>::widen(next.lo, x0);
-    RowLoad<T>::widen(next.hi, x1);
+    LaneRow x;
+    widen_row(next, x);
     if (r0 + STEP < rows) next.load(base + min(r0 + STEP + first, rows - 1) * D, R::HALF);
-    rms_norm_lane<D>(x0, x1, w0, w1, a.eps);
-    if (rotate) {
-      const float2 *row = cs[static_cast<uint32_t>(r) * a.q_div >> kNormDivBits] + w;
-      if (gptj)
-        rotate_pairs<true>(x0, x1, row, R::LPR);
-      else
-        rotate_pairs<false>(x0, x1, row, R::LPR);
-    }
-    if (r0 + first < rows) {
-      store8(base + r * D, x0);
-      store8(base + r * D + R::HALF, x1);
-    }
+    norm_rope_row<D>(x, weight, a.eps, rotate ? cs[static_cast<uint32_t>(r) * a.q_div >> kNormDivBits] : nullptr, w,
+                     gptj);
+    if (r0 + first < rows) store_row(base + r * D, R::HALF, x);
   }
 }
 

@@ -16,12 +16,12 @@ namespace photon {
 namespace {
 
 template <typename Tag, int D>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, D < 256 && sizeof(typename Tag::T) == 2 ? 4 : 2)
     qk_norm_rope_write_kernel(const __grid_constant__ NormRopeArgs a, unsigned int *err) {
   using T = typename Tag::T;
   using R = RopeRow<D>;
   constexpr int STEP = kNormThreads / R::LPR;
-  __shared__ float2 cs[kNormMaxTile][R::STRIDE];
+  __shared__ __align__(16) float cs[kNormMaxTile][R::STRIDE];
   __shared__ int64_t slots[kNormMaxTile];
   pdl_wait();
   pdl_launch_dependents();
@@ -39,14 +39,14 @@ __global__ void __launch_bounds__(kNormThreads)
   auto source = [&](int r) { return r < keys ? k + r * D : v + (min(r, rows - 1) - keys) * D; };
   RowLoad<T> next;
   next.load(source(first), R::HALF);
-  float w0[8], w1[8];
-  load_weights<T>(a.k_weight, w, R::HALF, w0, w1);
+  LaneRow weight;
+  load_weights<T>(a.k_weight, w, R::HALF, weight);
   if (static_cast<int>(threadIdx.x) < n) {
     const int64_t slot = a.slot_mapping[t0 + threadIdx.x];
     if (slot >= a.num_slots) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
     slots[threadIdx.x] = slot < a.num_slots ? slot : -1;
   }
-  if (rotate) rope_table_rows<D>(cs, a.positions + t0, n, a.turns, gptj, kNormThreads);
+  if (rotate) rope_table_rows<D>(cs, a.positions + t0, n, a.turns, gptj);
   __syncthreads();
   for (int r0 = 0; r0 < rows; r0 += STEP) {
     const int r = min(r0 + first, rows - 1);
@@ -60,20 +60,10 @@ __global__ void __launch_bounds__(kNormThreads)
     T *dst = static_cast<T *>(key ? a.k_cache : a.v_cache) +
              (((slot >> 4) * H + h) * kBlockSize + (slot & (kBlockSize - 1))) * D + 8 * w;
     if (__any_sync(0xffffffffu, key)) {
-      float x0[8], x1[8];
-      RowLoad<T>::widen(raw.lo, x0);
-      RowLoad<T>::widen(raw.hi, x1);
-      rms_norm_lane<D>(x0, x1, w0, w1, a.eps);
-      if (rotate) {
-        if (gptj)
-          rotate_pairs<true>(x0, x1, cs[t] + w, R::LPR);
-        else
-          rotate_pairs<false>(x0, x1, cs[t] + w, R::LPR);
-      }
-      if (live && key) {
-        store8(dst, x0);
-        store8(dst + R::HALF, x1);
-      }
+      LaneRow x;
+      widen_row(raw, x);
+      norm_rope_row<D>(x, weight, a.eps, rotate ? cs[t] : nullptr, w, gptj);
+      if (live && key) store_row(dst, R::HALF, x);
     }
     if (live && !key) raw.store(dst, R::HALF);
   }
