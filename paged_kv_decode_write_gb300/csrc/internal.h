@@ -215,7 +215,8 @@ cudaError_t launch_kv_cache_write_int8(NormRopeArgs a, bool norm, photon_dtype i
                                        unsigned int *err, cudaStream_t st);
 cudaError_t launch_kv_cache_read_int8(const CacheReadArgs &a, photon_dtype out_dt, unsigned int *err,
                                       cudaStream_t st);
-cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st);
+// *whole: every row is written, nothing to merge.
+cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st, bool *whole);
 cudaError_t launch_step_metadata(const StepMetaArgs &a, unsigned int *err, cudaStream_t st);
 
 // Every host-side check of photon_paged_attention_decode except the workspace

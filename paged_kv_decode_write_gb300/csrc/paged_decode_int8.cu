@@ -75,14 +75,43 @@ struct Int8Ring {
   static_assert(ST * PP <= 32, "a bit per page of the ring");
 };
 
-// TEAM: an item belongs to a CTA, whose warps take a share of its pages each
-// and meet in shared memory at its end (else every warp has items of its own).
-// They walk the same items, so their barriers match; a warp that gave up on a
-// copy still walks on to them.
-template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, bool TEAM>
+// Who takes an item.
+enum class Mode {
+  kWarps,    // every warp has items of its own
+  kTeams,    // a CTA, whose warps take a share of its pages each and meet in shared
+             // memory at its end.  They walk the same items, so their barriers match; a
+             // warp that gave up on a copy still walks on to them
+  kCluster,  // a cluster of CTAs, the whole context of one sequence and KV head: their
+             // teams' results meet in distributed shared memory, nothing is left to merge
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at p in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float load_cluster(const float *p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, Mode MODE>
 __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     paged_decode_int8_kernel(const DecodeArgs a, unsigned int *err) {
   using R = Int8Ring<D, PP, ST, NW>;
+  constexpr bool TEAM = MODE != Mode::kWarps, CLUSTER = MODE == Mode::kCluster;
   constexpr int HH = D / 64;
   constexpr int REC = R::REC;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -111,12 +140,31 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     }
   };
   auto next_item = [&](Walker &w) {
-    walker_next<BAL>(w, a, lane, err, workers);
-    if (w.valid) share(w);
+    if constexpr (CLUSTER) {
+      w.valid = false;
+    } else {
+      walker_next<BAL>(w, a, lane, err, workers);
+      if (w.valid) share(w);
+    }
   };
   Walker prod, w;  // the producer, ST steps ahead, and the consumer
-  walker_start<BAL>(prod, a, lane, err, TEAM ? blockIdx.x : blockIdx.x * NW + warp, workers);
-  if (prod.valid) share(prod);
+  if constexpr (CLUSTER) {
+    const int pair = static_cast<int>(blockIdx.x / cluster_size());
+    const int warps = static_cast<int>(cluster_size()) * NW;
+    prod.s = pair / a.num_kv_heads;
+    prod.h = pair - prod.s * a.num_kv_heads;
+    prod.ctx = prod.tok1 = balanced_ctx(a, prod.s, err);
+    const int pages = (prod.ctx + kBlockSize - 1) / kBlockSize;
+    const int part = ((pages + warps - 1) / warps + PP - 1) / PP * PP;
+    prod.pg0 = min(static_cast<int>(cluster_rank() * NW + warp) * part, pages);
+    prod.n_pages = min(part, pages - prod.pg0);
+    prod.page = prod.p = 0;
+    prod.P_s = 1;
+    prod.valid = true;
+  } else {
+    walker_start<BAL>(prod, a, lane, err, TEAM ? blockIdx.x : blockIdx.x * NW + warp, workers);
+    if (prod.valid) share(prod);
+  }
   w = prod;
 
   // Block-table window of the producer's item: lane j holds the record row of
@@ -134,7 +182,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
   if (prod.valid) ahead = table_entry(lane);
   // metadata only so far; pages, q and the workspace wait for the preceding kernel
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && a.seg_count)  // the merge's mode
+  if (!CLUSTER && blockIdx.x == 0 && threadIdx.x == 0 && a.seg_count)  // the merge's mode
     a.seg_count[static_cast<int64_t>(a.num_seqs) * a.num_q_heads] = BAL ? 1 : 0;
 
   // Starts the copies of the producer's next step into ring slot `slot`: the
@@ -173,7 +221,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
 
   bool gave_up = false;
   __shared__ float team_o[TEAM ? NW - 1 : 1][HH * 16][32];  // of warps 1 ..: accumulators,
-  __shared__ float team_ml[TEAM ? NW - 1 : 1][4][32];       // references and sums
+  __shared__ float team_ml[TEAM ? NW - 1 : 1][4][32];       // references and sums; then [0]: the team's
   while (w.valid) {
     // ---- a new item: the query group
     uint32_t qb[HH][4][2];     // q of head g, dims 16c + 4kt + {0,1}, {2,3} of each plane
@@ -411,6 +459,66 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
           for (int k = 0; k < NW - 1; ++k) y = fmaf(team_o[k][i][lane], f[k + 1][i & 1], y);
         }
       }
+      if constexpr (CLUSTER) {
+        const uint32_t C = cluster_size();
+        if (C > 1) {
+          if (warp == 0) {
+            __syncwarp();  // every lane has read the others' shares
+#pragma unroll
+            for (int i = 0; i < HH * 16; ++i) team_o[0][i][lane] = o[i / 16][i / 4 % 4][i % 4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              team_ml[0][j][lane] = m_ref[j];
+              team_ml[0][2 + j][lane] = l_run[j];
+            }
+          }
+          cluster_barrier();
+          // the first CTA's warps: 4 dims of head 2c + j each, dims 64 hh + 8g + 4t ..
+          for (int k = warp; cluster_rank() == 0 && k < 4 * HH; k += NW) {
+            const int hh = k >> 2, t = k >> 1 & 1, j = k & 1, head = 2 * c + j;
+            float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+            for (uint32_t q0 = 0; q0 < C; q0 += 4) {  // the CTAs in order, four at once
+              float m1[4], l1[4], x[4][4], top = M;
+#pragma unroll
+              for (uint32_t q = 0; q < 4; ++q) {
+                const uint32_t r = min(q0 + q, C - 1);
+                m1[q] = load_cluster(&team_ml[0][j][lane], r);
+                l1[q] = load_cluster(&team_ml[0][2 + j][lane], r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  x[q][i] = load_cluster(&team_o[0][16 * hh + 4 * (2 * t + (i >> 1)) + 2 * (i & 1) + j][lane], r);
+                if (q0 + q >= C) m1[q] = -INFINITY;
+                top = fmaxf(top, m1[q]);
+              }
+              const float f0 = M == -INFINITY ? 0.f : exp2_approx(M - top);
+              L *= f0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] *= f0;
+              M = top;
+#pragma unroll
+              for (uint32_t q = 0; q < 4; ++q) {
+                if (q0 + q >= C) continue;
+                const float f = m1[q] == -INFINITY ? 0.f : exp2_approx(m1[q] - M);  // a team without pages
+                L = fmaf(l1[q], f, L);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(x[q][i], f, v[i]);
+              }
+            }
+            if (head < G) {
+              const float f = L > 0.f || L != L ? 1.f / L : 0.f;
+              const int64_t at = (static_cast<int64_t>(w.s) * a.num_q_heads + w.h * G + head) * D + 64 * hh + 8 * g + 4 * t;
+              if (a.out_bf16)
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
+                    make_uint2(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f));
+              else
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) =
+                    make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+            }
+          }
+          cluster_barrier();  // the others' shared memory has been read
+          return;
+        }
+      }
       __syncthreads();  // read before the next item's shares are written
       if (warp > 0) {
         next_item(w);
@@ -504,7 +612,7 @@ template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, Int
 cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
   constexpr bool TEAM = FIT == Int8Fit::kTeams;
   constexpr int SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
-  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, TEAM>;
+  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, TEAM ? Mode::kTeams : Mode::kWarps>;
   static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -533,10 +641,84 @@ cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(NW * 32), SMEM, stream, la, err);
 }
 
+// Short steps: a cluster of up to eight CTAs takes the whole context of a sequence
+// and KV head and merges in distributed shared memory: no pieces bounded by the
+// partition size, no partials in memory, no second launch.  (Decode and merge ->
+// cluster: one context of 1024 4.7 -> 4.0 us, d 128 6.0 -> 5.1; four of 4096 9.8 -> 7.3
+// and 11.0 -> 9.5; 16 of 2048 11.1 -> 9.6 and 17.6 -> 14.0; 64 ragged ones of up to
+// 256 10.0 -> 5.1 and 14.6 -> 7.8, of up to 1024 14.3 -> 11.7 and 21.7 -> 20.3; 300 of up to 700
+// 36.2 -> 27.8 and 52.6 -> 43.2.)  What it costs is evenness: a warp's share follows the longest
+// context.  So it is taken while no warp has more than kClusterPages pages at the
+// declared longest one (16 ragged contexts of up to 4096, d 64, 16 pages: 13.7 against
+// 13.5), and, where the clusters leave more than half of the SMs idle, than 16 KB (8 of
+// up to 16384, 16 pages: 10.5 against 9.3; one of 8192, d 128, 8 pages: 9.4 against 8.4).
+constexpr int kClusterMax = 8, kClusterPages = 16, kClusterFewBytes = 16384;
+
+template <int D, int PP, int NW, bool SPLIT>
+cudaError_t launch_int8_cluster(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
+  constexpr int ST = 2, SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
+  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, 1, false, SPLIT, Mode::kCluster>;
+  static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  int occ = occupancy[dev].load(std::memory_order_relaxed);
+  if (occ == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, NW * 32, SMEM);
+    if (e != cudaSuccess) return e;
+    occ = occ > 0 ? occ : 1;
+    occupancy[dev].store(occ, std::memory_order_relaxed);
+  }
+  const int64_t sms = device_sm_count(), pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  const int64_t pages = (static_cast<int64_t>(a.ctx_cap) + kBlockSize - 1) / kBlockSize;
+  int ctas = kClusterMax;  // of a cluster: all resident at once, a step's pages at least per warp
+  while (ctas > 1 && (pairs * ctas > sms * occ || ctas * NW * PP > pages)) ctas /= 2;
+  const int64_t share = (pages + ctas * NW - 1) / (ctas * NW);
+  *taken = share <= kClusterPages && (2 * pairs * ctas >= sms || share * int8_record_bytes(D) <= kClusterFewBytes + 512);
+  if (!*taken || pairs == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ctas));
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, err);
+}
+
+// The cluster's width: 8 warps per CTA while the pairs of sequence and KV head are few,
+// so that a pair finds as many warps as possible; 4 where whole contexts per CTA fill
+// the GPU (d 64, 512 pairs of 600 tokens: 9.7 us, 12.8 with 8 warps); in d 128 steps of one
+// page and so three CTAs per SM for yet more pairs (512 pairs of 600 tokens: 16.3, 18.9 with two).
+template <int D, bool SPLIT>
+cudaError_t launch_int8_clusters(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
+  const int64_t sms = device_sm_count(), pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  if constexpr (D == 64) {
+    return pairs <= 3 * sms ? launch_int8_cluster<D, 2, 8, SPLIT>(a, err, stream, taken)
+                            : launch_int8_cluster<D, 2, 4, SPLIT>(a, err, stream, taken);
+  } else {
+    return pairs <= sms       ? launch_int8_cluster<D, 2, 8, SPLIT>(a, err, stream, taken)
+           : pairs <= 3 * sms ? launch_int8_cluster<D, 2, 4, SPLIT>(a, err, stream, taken)
+                              : launch_int8_cluster<D, 1, 4, SPLIT>(a, err, stream, taken);
+  }
+}
+
+// *whole: every row is written, nothing to merge.
 template <int D, bool BAL, bool SPLIT>
-cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t stream) {
+cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *whole) {
+  cudaError_t e = launch_int8_clusters<D, SPLIT>(a, err, stream, whole);
+  if (e != cudaSuccess || *whole) return e;
   bool taken = false;
-  cudaError_t e = launch_int8_kern<D, 2, 2, 4, 1, BAL, SPLIT, Int8Fit::kTeams>(a, err, stream, &taken);
+  e = launch_int8_kern<D, 2, 2, 4, 1, BAL, SPLIT, Int8Fit::kTeams>(a, err, stream, &taken);
   if (e != cudaSuccess || taken) return e;
   if constexpr (D == 64) {
     if constexpr (BAL) {
@@ -550,16 +732,18 @@ cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t str
 }
 
 template <int D>
-cudaError_t dispatch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
-  if (balanced_pieces(a)) return a.out_bf16 ? launch_int8<D, true, false>(a, err, st) : launch_int8<D, true, true>(a, err, st);
-  return a.out_bf16 ? launch_int8<D, false, false>(a, err, st) : launch_int8<D, false, true>(a, err, st);
+cudaError_t dispatch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st, bool *whole) {
+  if (balanced_pieces(a))
+    return a.out_bf16 ? launch_int8<D, true, false>(a, err, st, whole) : launch_int8<D, true, true>(a, err, st, whole);
+  return a.out_bf16 ? launch_int8<D, false, false>(a, err, st, whole) : launch_int8<D, false, true>(a, err, st, whole);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st) {
-  if (a.head_dim == 64) return dispatch_int8<64>(a, err, st);
-  if (a.head_dim == 128) return dispatch_int8<128>(a, err, st);
+cudaError_t launch_decode_partial_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st, bool *whole) {
+  *whole = false;
+  if (a.head_dim == 64) return dispatch_int8<64>(a, err, st, whole);
+  if (a.head_dim == 128) return dispatch_int8<128>(a, err, st, whole);
   return cudaErrorInvalidValue;
 }
 

@@ -893,8 +893,9 @@ int photon_paged_attention_decode_int8(const void *q, const void *kv_cache, cons
   unsigned int *err = error_word();
   if (!err) return PHOTON_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = cuda_status(launch_decode_partial_int8(p.args, err, st));
-  if (rc != PHOTON_OK || p.ws.total == 0) return rc;
+  bool whole = false;
+  rc = cuda_status(launch_decode_partial_int8(p.args, err, st, &whole));
+  if (rc != PHOTON_OK || p.ws.total == 0 || whole) return rc;
   return cuda_status(launch_decode_merge_fp4(p.args, st));
 }
 

@@ -62,9 +62,16 @@ def _runs(rng, nb, lens):
     return np.concatenate(out).astype(np.int64)
 
 
+# Declared longest contexts: the batch's own (short steps: clusters of CTAs), and one
+# that makes the same batch a long step's, which is cut into pieces and merged.
+DECLARED = [None, 40000]
+
+
 def _decode(pk, q, pool, bt, ctx, scale, out_dtype, part, max_ctx=None, extra_rows=0):
     torch = _torch()
     B, Hq, d = q.shape
+    if max_ctx is not None and bt.shape[1] * 16 < max_ctx:
+        bt = np.concatenate([bt, np.full((B, -(-max_ctx // 16) - bt.shape[1]), -1, np.int32)], 1)
     mc = int(max(max(ctx), 1)) if max_ctx is None else max_ctx
     n = pk.photon_paged_attention_workspace_size(B, Hq, d, mc, part)
     ws = torch.randint(0, 256, (max(n, 1),), dtype=torch.uint8, device="cuda") if n else None
@@ -342,11 +349,12 @@ CONTEXTS = [([1, 17, 600, 1500, 33, 0], 256), ([3000, 9, 700, 0, 16], 512),
             ([2500, 300], 4096)]
 
 
+@pytest.mark.parametrize("declared", DECLARED)
 @pytest.mark.parametrize("ctx,part", CONTEXTS)
 @pytest.mark.parametrize("H,G", [(8, 1), (8, 2), (8, 4), (4, 8), (1, 4), (3, 2)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-def test_decode_matches_the_oracle(ctx, part, H, G, d, out):
+def test_decode_matches_the_oracle(ctx, part, H, G, d, out, declared):
     torch = _torch()
     pk = ensure_built()
     rng = np.random.default_rng(sum(ctx) + H * G + d)
@@ -356,7 +364,7 @@ def test_decode_matches_the_oracle(ctx, part, H, G, d, out):
     q, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
     scale = d ** -0.5
     dt = torch.bfloat16 if out == "bf16" else torch.float32
-    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, dt, part, extra_rows=2)
+    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, dt, part, max_ctx=declared, extra_rows=2)
     ref = int8.paged_attention(q, pool, bt, ctx, scale)
     assert (got[len(ctx):] == -7.0).all()                  # rows behind the batch
     got = got[:len(ctx)].double().cpu().numpy()
@@ -369,10 +377,11 @@ def test_decode_matches_the_oracle(ctx, part, H, G, d, out):
     assert pk.photon_device_errors() == 0
 
 
+@pytest.mark.parametrize("declared", DECLARED)
 @pytest.mark.parametrize("qexp,vexp,scale", [(0, 0, -0.3), (100, 0, 2.0 ** -103), (-100, 0, 2.0 ** 97), (120, 0, 0.0), (123, 0, 2.0 ** -126),
                                              (0, 60, 0.125), (0, -100, 0.125), (0, 105, 0.125), (3, -60, -0.01), (-130, 0, 0.5)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_decode_is_scale_free(qexp, vexp, scale, d):
+def test_decode_is_scale_free(qexp, vexp, scale, d, declared):
     """q and V scales of any magnitude, blocks of zeros, a negative or zero softmax scale."""
     torch = _torch()
     pk = ensure_built()
@@ -385,15 +394,16 @@ def test_decode_is_scale_free(qexp, vexp, scale, d):
     pool[:, :, -16:-8] = sc.astype(np.float32).view(np.uint8)
     bt = _tables(rng, ctx, nb)
     q, qt = _storage(rng.standard_normal((3, H * G, d)) * 2.0 ** qexp, "bf16")
-    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, torch.float32, 64).double().cpu().numpy()
+    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, torch.float32, 64, max_ctx=declared).double().cpu().numpy()
     ref = int8.paged_attention(q, pool, bt, ctx, float(np.float32(scale)))
     kd, vd = int8.dequant(pool, d)
     assert np.isfinite(got).all()
     assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, scale, False, ref) + 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("declared", DECLARED)
 @pytest.mark.parametrize("jump", [-40, 40, 100])
-def test_decode_keeps_earlier_tokens_when_v_scales_jump(jump):
+def test_decode_keeps_earlier_tokens_when_v_scales_jump(jump, declared):
     """V of the later half of a context 2^jump times the earlier one's, whose
     weights dominate: nothing of either half is lost beyond the tolerance."""
     torch = _torch()
@@ -409,15 +419,16 @@ def test_decode_keeps_earlier_tokens_when_v_scales_jump(jump):
     pool[:, :, -16:-8] = sc.view(np.uint8)
     q, qt = _storage(rng.standard_normal((2, H * G, d)), "bf16")
     for part in (64, 1024):
-        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.125, torch.float32, part).double().cpu().numpy()
+        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.125, torch.float32, part, max_ctx=declared).double().cpu().numpy()
         ref = int8.paged_attention(q, pool, bt, ctx, 0.125)
         kd, vd = int8.dequant(pool, d)
         assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, 0.125, False, ref)).all()
 
 
+@pytest.mark.parametrize("declared", DECLARED)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("part", [32, 512])
-def test_decode_ignores_everything_past_the_context(d, part):
+def test_decode_ignores_everything_past_the_context(d, part, declared):
     """Any bytes in a page's tail rows and NaN scales in unused blocks leave every
     bit of the output as it was."""
     torch = _torch()
@@ -428,7 +439,7 @@ def test_decode_ignores_everything_past_the_context(d, part):
     pool = _random_pool(rng, nb, H, d)
     bt = _tables(rng, ctx, nb, width=32)
     _, qt = _storage(rng.standard_normal((len(ctx), H * G, d)), "bf16")
-    a = _decode(pk, qt, _dev(pool), bt, ctx, 0.2, torch.float32, part)
+    a = _decode(pk, qt, _dev(pool), bt, ctx, 0.2, torch.float32, part, max_ctx=declared)
     byte = int8.record_positions(d)
     used = np.zeros((nb, 16), bool)
     for s, c in enumerate(ctx):
@@ -438,14 +449,15 @@ def test_decode_ignores_everything_past_the_context(d, part):
         for w in range(2):
             pool[b][:, byte[w, r]] = rng.integers(0, 256, (H, d))
     pool[~used.any(1), :, -16:-8] = np.array([np.nan, np.inf], np.float32).view(np.uint8)
-    b_ = _decode(pk, qt, _dev(pool), bt, ctx, 0.2, torch.float32, part)
+    b_ = _decode(pk, qt, _dev(pool), bt, ctx, 0.2, torch.float32, part, max_ctx=declared)
     assert torch.equal(a, b_) and torch.isfinite(a).all()
     assert pk.photon_device_errors() == 0
 
 
+@pytest.mark.parametrize("declared", DECLARED)
 @pytest.mark.parametrize("part", [32, 1024])
 @pytest.mark.parametrize("which", [0, 1])
-def test_a_nan_block_makes_its_readers_nan(which, part):
+def test_a_nan_block_makes_its_readers_nan(which, part, declared):
     """Every head over a block with a NaN scale, in the sequences whose contexts
     reach it, and no other row."""
     torch = _torch()
@@ -458,12 +470,13 @@ def test_a_nan_block_makes_its_readers_nan(which, part):
     pool[bt[1, 3], 1, -16:-8].view(np.float32)[which] = np.nan
     _, qt = _storage(rng.standard_normal((4, H * G, d)), "bf16")
     for dt in (torch.bfloat16, torch.float32):
-        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.125, dt, part)
+        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.125, dt, part, max_ctx=declared)
         nan = torch.isnan(got).cpu().numpy()
         assert nan[1, G:].all() and nan.sum() == G * d
 
 
-def test_bad_block_ids_and_lengths_are_reported_and_skipped():
+@pytest.mark.parametrize("declared", DECLARED)
+def test_bad_block_ids_and_lengths_are_reported_and_skipped(declared):
     torch = _torch()
     pk = ensure_built()
     rng = np.random.default_rng(3)
@@ -475,7 +488,7 @@ def test_bad_block_ids_and_lengths_are_reported_and_skipped():
         bt[0, 3], bt[0, 7], bt[1, 0], bt[2, :3] = -1, nb, 2 ** 31 - 1, -5
         _, qt = _storage(rng.standard_normal((3, H * G, d)), "bf16")
         pk.photon_device_errors()
-        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.125, torch.float32, part)
+        got = _decode(pk, qt, _dev(pool), bt, ctx, 0.125, torch.float32, part, max_ctx=declared)
         assert pk.photon_device_errors() == pk.DEVERR_BLOCK_RANGE
         assert torch.isfinite(got).all() and (got[2] == 0).all()
         # what is left: the tokens of the good pages
@@ -499,7 +512,8 @@ def test_bad_block_ids_and_lengths_are_reported_and_skipped():
 @pytest.mark.parametrize("B,lo,hi,H,G,d,part,out", [
     (96, 256, 6000, 8, 4, 64, 512, "bf16"), (48, 16, 3000, 8, 2, 128, 128, "bf16"), (40, 500, 500, 8, 4, 64, 512, "bf16"),
     (60, 100, 1000, 8, 4, 128, 512, "bf16"), (3, 20000, 20000, 4, 8, 128, 256, "f32"), (1, 30000, 30000, 1, 8, 64, 512, "f32"),
-    (300, 1, 200, 8, 1, 64, 64, "f32"), (64, 5000, 8000, 8, 4, 64, 512, "f32"), (160, 3000, 5000, 4, 2, 128, 512, "bf16")])
+    (300, 1, 200, 8, 1, 64, 64, "f32"), (300, 1, 200, 8, 2, 128, 64, "bf16"), (20, 100, 900, 8, 4, 64, 64, "bf16"), (30, 300, 900, 8, 8, 128, 128, "f32"),
+    (1, 4096, 4096, 8, 4, 64, 64, "bf16"), (2, 5000, 5000, 1, 8, 128, 64, "f32"), (1, 8192, 8192, 4, 4, 64, 8192, "bf16"), (200, 2000, 9000, 2, 1, 64, 16384, "bf16"), (64, 5000, 8000, 8, 4, 64, 512, "f32"), (160, 3000, 5000, 4, 2, 128, 512, "bf16")])
 def test_decode_grids(B, lo, hi, H, G, d, part, out):
     """Batches that take each of the launch shapes, against attention over the
     dequantised values in fp64 on the GPU; twice the same bits."""
