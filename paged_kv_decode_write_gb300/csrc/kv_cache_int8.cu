@@ -118,6 +118,10 @@ struct Write8 {
   static constexpr int RPP = 32 / R::LPR, PASSES = kBlockSize / RPP;  // rows of a pass
   static_assert(RPP == 8 || RPP == 4, "head_dim 64 or 128");
 
+  // Unit u of a run is K (0) or V (1) of head (or heads) u / 2.  Every eighth unit is a
+  // warp's: the two take turns, K's rotation costs what would leave V's warps waiting.
+  __device__ __forceinline__ static int which(int u) { return (u ^ (u >> 3)) & 1; }
+
   __device__ __forceinline__ static unsigned char *record(const NormRopeArgs &a, int block, int h) {
     return static_cast<unsigned char *>(a.k_cache) +
            (static_cast<int64_t>(block) * a.num_kv_heads + h) * int8_record_bytes(D);
@@ -191,11 +195,11 @@ struct Write8 {
     float old;  // the block's scale so far
   };
 
-  // Starts unit u's loads (K of head u / 2, V where u is odd).  Rows that are not
-  // written take the run's first token: their values go nowhere.
+  // Starts unit u's loads.  Rows that are not written take the run's first token:
+  // their values go nowhere.
   __device__ __forceinline__ static void load(Unit &unit, const NormRopeArgs &a, const Run &run, int t0, int u,
                                               int lane) {
-    const T *x = static_cast<const T *>(u & 1 ? a.v : a.k) +
+    const T *x = static_cast<const T *>(which(u) ? a.v : a.k) +
                  (static_cast<int64_t>(t0) * a.num_kv_heads + (u >> 1)) * D + 8 * (lane % R::LPR);
     const int token = a.num_kv_heads * D;
 #pragma unroll
@@ -206,7 +210,7 @@ struct Write8 {
     }
     unit.old = run.written & 1u
                    ? 0.f
-                   : *reinterpret_cast<const float *>(record(a, run.block, u >> 1) + int8_scale_byte(D, u & 1));
+                   : *reinterpret_cast<const float *>(record(a, run.block, u >> 1) + int8_scale_byte(D, which(u)));
   }
 
   template <int WHICH>
@@ -224,6 +228,7 @@ struct Write8 {
       prepare<WHICH>(a, y[p], weight, w, cs[src < 0 ? run.any : src]);
       const float top = max_abs_row(y[p]);
       if (run.written >> (row0 + row_step(p)) & 1u) m = max_abs3(m, top, 0.f);
+      asm volatile("" ::: "memory");  // the next pass's table chunks are not fetched early: they would spill
     }
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // a NaN's bits are the largest
     const Scale s = new_scale(m, old);
@@ -258,9 +263,9 @@ struct Write8 {
   __device__ __forceinline__ static void load_single(Single &s, const NormRopeArgs &a, int64_t token, int block, int off,
                                                      int u, int lane) {
     const int h = min((u >> 1) * RPP + lane / R::LPR, a.num_kv_heads - 1);
-    s.raw.load(static_cast<const T *>(u & 1 ? a.v : a.k) + (token * a.num_kv_heads + h) * D + 8 * (lane % R::LPR),
+    s.raw.load(static_cast<const T *>(which(u) ? a.v : a.k) + (token * a.num_kv_heads + h) * D + 8 * (lane % R::LPR),
                R::HALF);
-    s.old = off == 0 ? 0.f : *reinterpret_cast<const float *>(record(a, block, h) + int8_scale_byte(D, u & 1));
+    s.old = off == 0 ? 0.f : *reinterpret_cast<const float *>(record(a, block, h) + int8_scale_byte(D, which(u)));
   }
 
   template <int WHICH>
@@ -354,15 +359,18 @@ __global__ void __launch_bounds__(kNormThreads, int8_write_ctas<typename Tag::T,
     }
   };
   typename W::Unit unit{};
-  typename W::Single ahead{};
-  bool have = false;  // `unit` holds the warp's first unit of the open tile's runs of several tokens
+  // `unit` holds the warp's first unit of the open tile's runs of several tokens; else,
+  // as its first row, that of the runs of one token
+  bool have = false;
   auto load_single = [&](int j) {  // the warp's j-th unit of the runs of one token
+    typename W::Single s;
     const int n = 2 * W::groups(a);
     uint32_t left = singles;
     for (; j >= n; j -= n) left &= left - 1;
     const int i = __ffs(left) - 1;
-    W::load_single(ahead, a, static_cast<int64_t>(t0) - 1 + i, __shfl_sync(0xffffffffu, block, i),
+    W::load_single(s, a, static_cast<int64_t>(t0) - 1 + i, __shfl_sync(0xffffffffu, block, i),
                    __shfl_sync(0xffffffffu, off, i), j, lane);
+    return s;
   };
   // Opens the CTA's next tile in which a run begins, the same in every warp, and
   // starts the warp's first loads there.
@@ -397,7 +405,9 @@ __global__ void __launch_bounds__(kNormThreads, int8_write_ctas<typename Tag::T,
         take_run();
         W::load(unit, a, run, t0, warp, lane);
       } else if (warp < __popc(singles) * 2 * W::groups(a)) {
-        load_single(warp);
+        const typename W::Single s = load_single(warp);
+        unit.raw[0] = s.raw;
+        unit.old = s.old;
       }
       return true;
     }
@@ -407,22 +417,23 @@ __global__ void __launch_bounds__(kNormThreads, int8_write_ctas<typename Tag::T,
   if (!next_tile()) return;
   for (int buf = 0;; buf ^= 1) {
     if (rotate) {
-      rope_table_rows<D>(cs[buf] + (first - 1), pos, first, last + 1 - first, a.turns,
-                         a.rope_style == PHOTON_ROPE_GPTJ);
+      rope_table_rows<D>(cs[buf] + (first - 1), last + 1 - first, a.turns, a.rope_style == PHOTON_ROPE_GPTJ,
+                         [&](int t) { return __shfl_sync(0xffffffffu, pos, first + t); });
       __syncthreads();  // the table of the tile before last is free: its readers passed the barrier since
     }
     const int n1 = 2 * W::groups(a);
     for (int j = warp; j < __popc(singles) * n1; j += kInt8Warps) {
-      if (j != warp || have) load_single(j);
+      typename W::Single s{unit.raw[0], unit.old};
+      if (j != warp || have) s = load_single(j);
       uint32_t left = singles;
       int u = j;
       for (; u >= n1; u -= n1) left &= left - 1;
       const int i = __ffs(left) - 1;
       const int b = __shfl_sync(0xffffffffu, block, i), o = __shfl_sync(0xffffffffu, off, i);
-      if (u & 1)
-        W::template write_single<1>(a, ahead, b, o, u >> 1, lane, cs[buf][i - 1]);
+      if (W::which(u))
+        W::template write_single<1>(a, s, b, o, u >> 1, lane, cs[buf][i - 1]);
       else
-        W::template write_single<0>(a, ahead, b, o, u >> 1, lane, cs[buf][i - 1]);
+        W::template write_single<0>(a, s, b, o, u >> 1, lane, cs[buf][i - 1]);
     }
     bool more = true;  // there is another tile
     if (!have) {
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(kNormThreads, int8_write_ctas<typename Tag::T,
           W::load(unit, a, run, t0, u, lane);
         else
           more = next_tile();
-        if (u0 & 1)
+        if (W::which(u0))
           W::template write<1>(a, now, u0 >> 1, lane, y, old, cs[buf]);
         else
           W::template write<0>(a, now, u0 >> 1, lane, y, old, cs[buf]);

@@ -11,9 +11,9 @@
 // Angles are 64-bit fractions of a turn: pos * F mod 2^64, F = 2^64 theta^(-2i/d)
 // / 2 pi rounded, is reduced exactly by the integer wrap, so far positions lose
 // nothing (F carries an fp64 frequency's 53 bits).  The nearest quarter turn
-// comes off exactly as well; the rest, at most an eighth of a turn, goes through
-// sincospif from its leading 32 bits: |error| <= 2^-29 of the angle's radians
-// plus the function's two units in the last place, 2^-23 absolute.
+// comes off exactly as well; the rest, at most an eighth of a turn, is taken from its
+// leading 32 bits (2^-29 radians) to the Taylor series of sine and cosine at 0, whose
+// terms past x^9 and x^10 are below 2^-29 there: with the roundings within 2^-23.
 #pragma once
 
 #include "row_lanes.cuh"
@@ -67,47 +67,48 @@ struct RopeRow {
   }
 };
 
-// (cos, sin) of the fraction turn / 2^64 of a turn.
-__device__ __forceinline__ float2 cos_sin_of_turn(unsigned long long turn) {
-  const unsigned up = static_cast<unsigned>(turn >> 32) + 0x20000000u;  // nearest quarter: the top two bits
-  const int rest = static_cast<int>(up & 0x3fffffffu) - 0x20000000;     // 2^-32 turn, |rest| <= 2^29
-  float s, c;
-  sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);
-  const unsigned quarter = up >> 30;
-  float2 r = (quarter & 1u) ? make_float2(-s, c) : make_float2(c, s);
-  if (quarter & 2u) r = make_float2(-r.x, -r.y);
-  return r;
+// (cos, sin) of a fraction of a turn, in units of 2^-32.
+__device__ __forceinline__ float2 cos_sin_of_turn(unsigned turn) {
+  const unsigned up = turn + 0x20000000u;                            // nearest quarter: the top two bits
+  const int rest = static_cast<int>(up & 0x3fffffffu) - 0x20000000;  // |rest| <= 2^29
+  const float x = static_cast<float>(rest) * static_cast<float>(6.283185307179586476925286766559 * 0x1p-32);
+  const float x2 = x * x;
+  float s = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+  s = fmaf(x2, s, 1.f / 120.f);
+  s = fmaf(x2, s, -1.f / 6.f);
+  s = fmaf(x * x2, s, x);
+  float c = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+  c = fmaf(x2, c, -1.f / 720.f);
+  c = fmaf(x2, c, 1.f / 24.f);
+  c = fmaf(x2, c, -0.5f);
+  c = fmaf(x2, c, 1.f);
+  // a quarter turn on: (c, s) -> (-s, c)
+  const bool odd = up & 0x40000000u;
+  const unsigned flip = up & 0x80000000u;
+  const float u = odd ? -s : c, v = odd ? c : s;
+  return make_float2(__uint_as_float(__float_as_uint(u) ^ flip), __uint_as_float(__float_as_uint(v) ^ flip));
 }
 
-// Table rows 0 .. n - 1 of the positions pos[0 .. n - 1], by all threads of the CTA.
-template <int D>
-__device__ __forceinline__ void rope_table_rows(float (*cs)[RopeRow<D>::STRIDE], const int32_t *pos, int n,
-                                                const unsigned long long *turns, bool gptj) {
-  using R = RopeRow<D>;
-  for (int i = threadIdx.x; i < n * R::HALF; i += kNormThreads) {
-    const int t = i / R::HALF, pair = i % R::HALF;
-    const float2 v =
-        cos_sin_of_turn(static_cast<unsigned long long>(static_cast<long long>(pos[t])) * turns[pair]);
-    float *at = cs[t] + R::at(pair, gptj);
-    at[0] = v.x;
-    at[2] = v.y;
-  }
+// The leading 32 bits of pos * turns mod 2^64.
+__device__ __forceinline__ unsigned turn_of(int pos, unsigned long long turns) {
+  const unsigned p = static_cast<unsigned>(pos);
+  return __umulhi(p, static_cast<unsigned>(turns)) + p * static_cast<unsigned>(turns >> 32);
 }
 
-// The same of positions that lie in a warp's lanes, pos of lane `lane0 + t` for row
-// t: with D >= 64 every 32 entries belong to one token.
-template <int D>
-__device__ __forceinline__ void rope_table_rows(float (*cs)[RopeRow<D>::STRIDE], int pos, int lane0, int n,
-                                                const unsigned long long *turns, bool gptj) {
+// Table rows 0 .. n - 1, by all threads of the CTA: a thread keeps its pair.
+// position(t): that of row t, asked for by whole warps where D >= 64.
+template <int D, typename Position>
+__device__ __forceinline__ void rope_table_rows(float (*cs)[RopeRow<D>::STRIDE], int n,
+                                                const unsigned long long *turns, bool gptj, Position position) {
   using R = RopeRow<D>;
-  static_assert(R::HALF % 32 == 0, "a warp's entries are one token's");
-  for (int i = threadIdx.x; i < n * R::HALF; i += kNormThreads) {
-    const int t = i / R::HALF, pair = i % R::HALF;
-    const int p = __shfl_sync(0xffffffffu, pos, lane0 + t);
-    const float2 v = cos_sin_of_turn(static_cast<unsigned long long>(static_cast<long long>(p)) * turns[pair]);
-    float *at = cs[t] + R::at(pair, gptj);
-    at[0] = v.x;
-    at[2] = v.y;
+  const int pair = threadIdx.x % R::HALF;
+  const unsigned long long turn = turns[pair];
+  const int at = R::at(pair, gptj);
+#pragma unroll 1
+  for (int t = threadIdx.x / R::HALF; t < n; t += kNormThreads / R::HALF) {
+    const float2 v = cos_sin_of_turn(turn_of(position(t), turn));
+    cs[t][at] = v.x;
+    cs[t][at + 2] = v.y;
   }
 }
 
@@ -125,7 +126,8 @@ __device__ __forceinline__ void rotate_row(LaneRow &x, const float *cs, int w, b
       q = make_float2(fmaf(q.x, t.y, -(q.y * t.w)), fmaf(q.y, t.y, q.x * t.w));
     } else {
       const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), u = x.a[j], v = x.b[j];
-      x.a[j] = __ffma2_rn(u, c, __fmul2_rn(v, make_float2(-t.z, -t.w)));
+      const float2 vs = __fmul2_rn(v, s);
+      x.a[j] = __ffma2_rn(u, c, make_float2(-vs.x, -vs.y));
       x.b[j] = __ffma2_rn(v, c, __fmul2_rn(u, s));
     }
   }
@@ -198,7 +200,7 @@ __device__ __forceinline__ void norm_rope_q_tile(const NormRopeArgs &a, int tile
   next.load(base + min(first, rows - 1) * D, R::HALF);
   LaneRow weight;
   load_weights<T>(a.q_weight, w, R::HALF, weight);
-  if (rotate) rope_table_rows<D>(cs, a.q_positions + t0, n, a.turns, gptj);
+  if (rotate) rope_table_rows<D>(cs, n, a.turns, gptj, [&](int t) { return a.q_positions[t0 + t]; });
   __syncthreads();
   for (int r0 = 0; r0 < rows; r0 += STEP) {  // lanes past the last row repeat it, for the shuffles
     const int r = min(r0 + first, rows - 1);

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kNormThreads, D < 256 && sizeof(typename Tag::
     if (slot >= a.num_slots) atomicOr(err, PHOTON_DEVERR_SLOT_RANGE);
     slots[threadIdx.x] = slot < a.num_slots ? slot : -1;
   }
-  if (rotate) rope_table_rows<D>(cs, a.positions + t0, n, a.turns, gptj);
+  if (rotate) rope_table_rows<D>(cs, n, a.turns, gptj, [&](int t) { return a.positions[t0 + t]; });
   __syncthreads();
   for (int r0 = 0; r0 < rows; r0 += STEP) {
     const int r = min(r0 + first, rows - 1);
