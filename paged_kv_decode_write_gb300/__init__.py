@@ -158,13 +158,18 @@ def _check(status: int, what: str):
 
 # ---- device-tensor marshalling ---------------------------------------------
 
+_dt_codes = {}  # torch dtype -> code, filled on first use (an import statement costs 0.3 us a call)
+
+
 def _dt(t) -> int:
+    code = _dt_codes.get(t.dtype)
+    if code is not None:
+        return code
     import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"storage dtype must be float32 or bfloat16, got {t.dtype}")
+    _dt_codes.update({torch.float32: F32, torch.bfloat16: BF16})
+    if t.dtype not in _dt_codes:
+        raise TypeError(f"storage dtype must be float32 or bfloat16, got {t.dtype}")
+    return _dt_codes[t.dtype]
 
 
 def _p(t):
@@ -444,8 +449,8 @@ def photon_paged_attention_decode_fp4(q, kv_cache, block_tables, context_lens, s
 # ---- q/k norms in the write, 8-bit KV cache with a scale per block and head ------
 
 def _norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight):
-    """The leading arguments of the writes with norms (q and its companions None:
-    no query rows)."""
+    """k's shape and the leading arguments of the writes with norms (q and its
+    companions None: no query rows)."""
     shape, dtype = _rows("k", k), k.dtype
     T, H, d = shape
     i32 = torch.int32
@@ -458,10 +463,10 @@ def _norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weig
             raise ValueError(f"q must have head_dim {d}, got {dq}")
         head = (_arg("q", q, dtype, None, dev), _arg("q_positions", q_positions, i32, (Tq,), dev), Tq, Hq)
         qw = _arg("q_weight", q_weight, dtype, (d,), dev)
-    return head + (_arg("k", k, dtype, None, dev), _arg("v", v, dtype, shape, dev),
-                   _arg("positions", positions, i32, (T,), dev),
-                   _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), qw,
-                   _arg("k_weight", k_weight, dtype, (d,), dev))
+    return shape, head + (_arg("k", k, dtype, None, dev), _arg("v", v, dtype, shape, dev),
+                          _arg("positions", positions, i32, (T,), dev),
+                          _arg("slot_mapping", slot_mapping, torch.int64, (T,), dev), qw,
+                          _arg("k_weight", k_weight, dtype, (d,), dev))
 
 
 def photon_qk_norm_rope_kv_cache_write(q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight, eps,
@@ -469,16 +474,15 @@ def photon_qk_norm_rope_kv_cache_write(q, q_positions, k, v, positions, slot_map
     """RMS norms of q [Tq, H_q, d] (weights q_weight [d]) and k [T, H_kv, d]
     (k_weight [d]) per head, their rotation, and the write of k and v; q in
     place.  All of one type, float32 or bfloat16; q None: keys only."""
-    T, H, d = _rows("k", k)
     torch, dev, st = _place("k", k, stream)
+    (T, H, d), head = _norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight)
     shape, dtype = k_cache.shape, k.dtype
     if len(shape) != 4 or shape[1] != H or shape[3] != d:
         raise ValueError(f"k_cache must be [num_blocks, {H}, block_size, {d}], got {tuple(shape)}")
     style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
     _check(lib().photon_qk_norm_rope_kv_cache_write(
-        *_norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight), float(eps),
-        _arg("k_cache", k_cache, dtype, None, dev), _arg("v_cache", v_cache, dtype, shape, dev), T, H, d, shape[2],
-        shape[0], _dt(k), float(rope_theta), style, st), "photon_qk_norm_rope_kv_cache_write")
+        *head, float(eps), _arg("k_cache", k_cache, dtype, None, dev), _arg("v_cache", v_cache, dtype, shape, dev),
+        T, H, d, shape[2], shape[0], _dt(k), float(rope_theta), style, st), "photon_qk_norm_rope_kv_cache_write")
 
 
 def photon_kv_cache_int8_record_bytes(head_dim: int) -> int:
@@ -507,13 +511,12 @@ def photon_qk_norm_rope_kv_cache_write_int8(q, q_positions, k, v, positions, slo
                                             kv_cache, rope_theta, rope_style="neox", stream=None):
     """photon_qk_norm_rope_kv_cache_write into an 8-bit pool (see
     photon_kv_cache_write_int8)."""
-    T, H, d = _rows("k", k)
     torch, dev, st = _place("k", k, stream)
+    (T, H, d), head = _norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight)
     pool, nb = _pool(kv_cache, H, d, dev, torch.uint8, 32 * d + 16)
     style = _ROPE[rope_style] if isinstance(rope_style, str) else int(rope_style)
     _check(lib().photon_qk_norm_rope_kv_cache_write_int8(
-        *_norm_args(torch, dev, q, q_positions, k, v, positions, slot_mapping, q_weight, k_weight), float(eps), pool,
-        T, H, d, 16, nb, _dt(k), float(rope_theta), style, st), "photon_qk_norm_rope_kv_cache_write_int8")
+        *head, float(eps), pool, T, H, d, 16, nb, _dt(k), float(rope_theta), style, st), "photon_qk_norm_rope_kv_cache_write_int8")
 
 
 def photon_kv_cache_read_int8(kv_cache, slot_mapping, k, v, stream=None):

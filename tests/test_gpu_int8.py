@@ -149,6 +149,128 @@ def test_long_batches_equal_the_oracle(T, H, d, run):
     assert np.array_equal(pool.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("H,d", [(8, 64), (3, 64), (2, 128), (5, 128)])
+@pytest.mark.parametrize("pieces", [40, 900])
+def test_runs_of_every_length_next_to_each_other(H, d, pieces):
+    """Single tokens, chunks, whole blocks and long prompts mixed, with skipped
+    tokens between them: every path of a tile beside the others, bit for bit."""
+    pk = ensure_built()
+    rng = np.random.default_rng(pieces + H)
+    lens = rng.choice([1, 1, 1, 2, 5, 15, 16, 17, 33, 64], pieces).tolist()
+    nb = sum(n // 16 + 2 for n in lens)
+    slots, at = [], 0
+    for n in lens:
+        base = int(rng.choice([0, 0, rng.integers(0, 16)]))
+        slots.append(at * 16 + base + np.arange(n))
+        at += (base + n - 1) // 16 + 1
+        if rng.random() < 0.2:
+            slots.append(np.full(int(rng.integers(1, 20)), -1))
+    slots = np.concatenate(slots).astype(np.int64)
+    perm = rng.permutation(nb)
+    slots = np.where(slots < 0, -1, perm[np.maximum(slots, 0) // 16] * 16 + slots % 16)
+    T = len(slots)
+    k, kt = _storage(rng.standard_normal((T, H, d)), "bf16")
+    v, vt = _storage(rng.standard_normal((T, H, d)) * 2, "bf16")
+    want = _random_pool(rng, nb, H, d)
+    pool = _dev(want.copy())
+    pk.photon_kv_cache_write_int8(kt, vt, _dev(np.zeros(T, np.int32)), _dev(slots), pool, 1e6, "none")
+    int8.write_rows(oracle.to_f64(k), slots, want, 0, d)
+    int8.write_rows(oracle.to_f64(v), slots, want, 1, d)
+    assert np.array_equal(pool.cpu().numpy(), want)
+
+
+def test_blocks_past_32_bits_of_the_pool():
+    """Write, read and decode at the end of a pool of more than 2^32 bytes."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(8)
+    d, H, nb = 128, 1, 1100000
+    pool = torch.empty(nb, H, 32 * d + 16, dtype=torch.uint8, device="cuda")
+    T = 40
+    bt = (nb - 1 - np.arange(3))[None].astype(np.int32)
+    slots = (bt[0, np.arange(T) // 16].astype(np.int64) * 16 + np.arange(T) % 16)
+    k, kt = _storage(rng.standard_normal((T, H, d)), "bf16")
+    pos = _dev(np.zeros(T, np.int32))
+    pk.photon_kv_cache_write_int8(kt, kt, pos, _dev(slots), pool, 1e4, "none")
+    small = np.zeros((3, H, 32 * d + 16), np.uint8)
+    for w in range(2):
+        int8.write_rows(oracle.to_f64(k), (2 - np.arange(T) // 16) * 16 + np.arange(T) % 16, small, w, d)
+    assert np.array_equal(pool[nb - 3:].cpu().numpy()[..., :-8], small[..., :-8])
+    kb, vb = (torch.empty(T, H, d, device="cuda") for _ in range(2))
+    pk.photon_kv_cache_read_int8(pool, _dev(slots), kb, vb)
+    want = int8.dequant(small, d)[0][2 - np.arange(T) // 16, :, np.arange(T) % 16].astype(np.float32)
+    assert np.array_equal(kb.cpu().numpy(), want) and torch.equal(kb, vb)
+    q, qt = _storage(rng.standard_normal((1, 4, d)), "bf16")
+    for declared in DECLARED:
+        got = _decode(pk, qt, pool, bt, [T], d ** -0.5, torch.float32, 64, max_ctx=declared).double().cpu().numpy()
+        ref = int8.paged_attention(q, small, np.array([[2, 1, 0]], np.int32), [T], d ** -0.5)
+        kd, vd = int8.dequant(small, d)
+        assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, [T], d ** -0.5, False, ref)).all()
+    assert pk.photon_device_errors() == 0
+
+
+def test_many_queries_beside_the_write():
+    """So many query rows that they get a launch of their own: all of them, and
+    the codes, as the bf16 write's norms give them."""
+    torch = _torch()
+    pk = ensure_built()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T, H, Hq, d, nb = 8200, 2, 32, 64, 520
+    mk = lambda h: torch.randn(T, h, d, generator=gen, device="cuda").bfloat16()
+    q, k, v = mk(Hq), mk(H), mk(H)
+    wq, wk = (1 + 0.2 * torch.randn(d, generator=gen, device="cuda") for _ in range(2))
+    wq, wk = wq.bfloat16(), wk.bfloat16()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 3
+    slots = torch.arange(T, device="cuda") + 5
+    pool = torch.zeros(nb, H, 32 * d + 16, dtype=torch.uint8, device="cuda")
+    kc, vc = (torch.zeros(nb, H, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q1, q2 = q.clone(), q.clone()
+    pk.photon_qk_norm_rope_kv_cache_write_int8(q1, pos, k, v, pos, slots, wq, wk, 1e-6, pool, 1e6)
+    pk.photon_qk_norm_rope_kv_cache_write(q2, pos, k, v, pos, slots, wq, wk, 1e-6, kc, vc, 1e6)
+    assert torch.equal(q1, q2)
+    kb, vb = (torch.empty(T, H, d, device="cuda") for _ in range(2))
+    pk.photon_kv_cache_read_int8(pool, slots, kb, vb)
+    sc = torch.from_numpy(int8.scales(pool.cpu().numpy()).copy()).cuda()[slots // 16]      # [T, H, 2]
+    rows = kc[slots // 16, :, slots % 16].float()
+    # half a step of the codes, and of the bf16 rows that they are compared with
+    assert ((kb - rows).abs() <= 0.5 * sc[..., :1] * (1 + 2.0 ** -10) + rows.abs() * 2.0 ** -8).all()
+    assert ((vb - v.float()).abs() <= 0.5 * sc[..., 1:] * (1 + 2.0 ** -10)).all()
+
+
+def test_writes_on_another_stream_captured_and_replayed():
+    """The same bytes on a side stream and from a graph, replayed with new rows;
+    nothing is allocated."""
+    torch = _torch()
+    pk = ensure_built()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    T, H, d, nb = 70, 4, 64, 12
+    k, v = (torch.randn(T, H, d, generator=gen, device="cuda") for _ in range(2))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda") + 7
+    start = _dev(_random_pool(np.random.default_rng(4), nb, H, d))
+    call = lambda pool, **kw: pk.photon_kv_cache_write_int8(k, v, pos, slots, pool, 1e4, **kw)
+    a, b, c = start.clone(), start.clone(), start.clone()
+    call(a)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(b, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    call(c)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(c)
+    for sign in (1, -1, 3):
+        k.mul_(sign)
+        c.copy_(start)
+        g.replay()
+        a.copy_(start)
+        call(a)
+        assert torch.equal(a, c)
+
+
 def _check_rotated(got, before, y, slots, d, which):
     """Codes and scales of fp32-rotated rows against fp64 rows y.  A value is off
     by at most 2^-19 of its pair's length, which is at most sqrt 2 m: the scale

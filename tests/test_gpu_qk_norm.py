@@ -191,6 +191,25 @@ def test_equals_norm_then_rotation_then_write():
         assert (x - y).abs().max().item() <= 2 * 1.5 * 128 ** 0.5 * 2.0 ** -19
 
 
+def test_pools_past_32_bits():
+    """Slots at the end of pools of more than 2^31 elements."""
+    torch = _torch()
+    pk = ensure_built()
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    T, H, d, nb = 37, 2, 128, 600000
+    k, v = (torch.randn(T, H, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    out = []
+    for blocks in (nb, 3):
+        kc, vc = (torch.empty(blocks, H, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        slots = (blocks - 3) * 16 + torch.arange(T, device="cuda")
+        pk.photon_qk_norm_rope_kv_cache_write(None, None, k, v, pos, slots, None, w, 1e-6, kc, vc, 1e4)
+        out.append([c[-3:].transpose(1, 2).reshape(48, H, d)[:T].clone() for c in (kc, vc)])
+    assert all(torch.equal(a, b) for a, b in zip(*out)) and torch.equal(out[0][1], v)
+    assert pk.photon_device_errors() == 0
+
+
 def test_refusals():
     torch = _torch()
     pk = ensure_built()

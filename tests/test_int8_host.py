@@ -71,6 +71,79 @@ def test_norm_rope_has_its_invariants():
     assert np.allclose(int8.norm_rope(x, None, 1.0, np.zeros(5), 1e4), x)
 
 
+# ---- models of the kernels' arithmetic -------------------------------------------
+
+def _f(x):
+    return np.float32(x)
+
+
+def _fma(a, b, c):
+    """fp32 fma of arrays: the product is exact in long double, the sum rounded there to 64 bits first."""
+    return (a.astype(np.longdouble) * np.longdouble(b) + np.asarray(c, np.longdouble)).astype(np.float32)
+
+
+def test_the_corrected_product_is_the_quotient_by_127():
+    """q = m fl(1/127), corrected once by its exact residual, for every mantissa
+    and exponents from the least scale to the largest float."""
+    mant = np.arange(1 << 23, dtype=np.uint32)
+    inv = _f(1) / _f(127)
+    for e in (34, 127, 253):
+        m = ((np.uint32(e) << np.uint32(23)) | mant).view(np.float32)
+        q = m * inv
+        assert np.array_equal(_fma(_fma(q, -127.0, m), inv, q), m / _f(127))
+
+
+def test_row_divisions_are_exact():
+    """row * ceil(2^28 / heads) >> 28 is row / heads for the rows of 8 tokens."""
+    for heads in list(range(1, 70)) + [96, 127, 128, 1000, 1024, 4095, 4096]:
+        div = ((1 << 28) + heads - 1) // heads
+        r = np.arange(8 * heads, dtype=np.uint64)
+        assert int((r * np.uint64(div)).max()) < 2 ** 32
+        assert np.array_equal((r * np.uint64(div)) >> np.uint64(28), r // np.uint64(heads))
+
+
+def test_rotation_table_is_within_its_bound():
+    """cos and sin of a fraction of a turn: the nearest quarter off exactly, the
+    rest by Taylor series in fp32, within 2^-23 for fractions of every kind."""
+    rng = np.random.default_rng(0)
+    turn = np.concatenate([rng.integers(0, 2 ** 32, 1 << 20, dtype=np.uint64), np.arange(0, 2 ** 32, 2 ** 13, dtype=np.uint64),
+                           (np.arange(9, dtype=np.uint64) * 2 ** 29 + np.arange(-3, 4)[:, None].astype(np.uint64)).ravel() & 0xFFFFFFFF])
+    up = (turn + 0x20000000) & 0xFFFFFFFF
+    rest = (up & 0x3FFFFFFF).astype(np.int64) - 0x20000000
+    x = rest.astype(np.float32) * _f(2 * np.pi * 2.0 ** -32)
+    x2 = x * x
+    s = _fma(x2, _f(1 / 362880), _f(-1 / 5040))
+    for k in (1 / 120, -1 / 6):
+        s = _fma(x2, s.astype(np.longdouble), _f(k))
+    s = _fma(x * x2, s.astype(np.longdouble), x)
+    c = _fma(x2, _f(-1 / 3628800), _f(1 / 40320))
+    for k in (-1 / 720, 1 / 24, -0.5, 1.0):
+        c = _fma(x2, c.astype(np.longdouble), _f(k))
+    quarter = (up >> 30).astype(int)
+    sign = np.where(quarter >= 2, -1, 1)
+    cos, sin = np.where(quarter & 1, -s, c) * sign, np.where(quarter & 1, c, s) * sign
+    ang = turn.astype(np.float64) * (2 * np.pi / 2 ** 32)
+    assert np.abs(cos - np.cos(ang)).max() <= 2.0 ** -23 and np.abs(sin - np.sin(ang)).max() <= 2.0 ** -23
+
+
+def test_turns_of_far_positions():
+    """The leading half of pos * F mod 2^64, taken from two 32-bit products."""
+    rng = np.random.default_rng(1)
+    for _ in range(2000):
+        f, pos = int(rng.integers(0, 2 ** 63)) * 2 + int(rng.integers(0, 2)), int(rng.integers(0, 2 ** 31))
+        lead = ((pos * (f & 0xFFFFFFFF) >> 32) + pos * (f >> 32)) & 0xFFFFFFFF
+        assert lead == (pos * f % 2 ** 64) >> 32
+
+
+def test_codes_are_the_low_bytes_of_one_fma():
+    """fma(y, r, 1.5 * 2^23 + 128): its low byte is the code + 128, halves to even."""
+    rng = np.random.default_rng(2)
+    y = np.concatenate([rng.uniform(-127, 127, 20000), np.arange(-254, 255) / 2]).astype(np.float32)
+    for r in (_f(1), _f(0.37), _f(1 / 3)):
+        q = _fma(y, r, _f(12582912 + 128))
+        assert np.array_equal((q.view(np.uint32) & 0xFF).astype(int) - 128, int8.round_codes(y, r))
+
+
 P = ctypes.c_void_p
 
 
