@@ -83,14 +83,11 @@ struct NormRopeArgs {
   int32_t num_kv_heads;
   int32_t rope_style;
   float eps;
-  uint32_t q_div;   // 2^28 / heads, rounded up: row / heads = row * div >> 28
-  uint32_t kv_div;
   unsigned long long turns[kMaxRopePairs];
   int32_t q_tiles;  // CTAs that take query tiles (the first ones)
   int32_t q_tile_log2;
   int32_t tile_log2;
 };
-constexpr int kNormMaxHeads = 4096;  // (8 tokens x heads)^2 < 2^28 / 8 keeps that division exact
 
 // Read of 4-bit and 8-bit cache rows back to a floating type.
 struct CacheReadArgs {

@@ -136,14 +136,12 @@ struct Write8 {
   __device__ __forceinline__ static void prepare(const NormRopeArgs &a, LaneRow &y, const RowLoad<T> &weight, int w,
                                                  const float *row) {
     if constexpr (!WHICH) {
-      const bool gptj = a.rope_style == PHOTON_ROPE_GPTJ;
-      if (a.rope_style == PHOTON_ROPE_NONE) row = nullptr;
+      const bool gptj = a.rope_style == PHOTON_ROPE_GPTJ, rotate = a.rope_style != PHOTON_ROPE_NONE;
+      const RowAt<D> at{row, w};
       if constexpr (NORM) {
-        LaneRow f;
-        widen_row(weight, f);
-        norm_rope_row<D>(y, f, a.eps, row, w, gptj);
-      } else if (row) {
-        rotate_row<D>(y, row, w, gptj);
+        norm_rope_row<T, D>(y, weight, a.eps, rotate, at, gptj);
+      } else if (rotate) {
+        rotate_row(y, at, gptj);
       }
     }
   }
@@ -220,7 +218,7 @@ struct Write8 {
     const bool anew = run.written & 1u;
     float m = 0.f;
     RowLoad<T> weight;
-    if (NORM && !WHICH) weight.load(static_cast<const T *>(a.k_weight) + 8 * w, R::HALF);
+    if (NORM && !WHICH) weight = load_weights<T>(a.k_weight, w, R::HALF);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       if (!(run.written & rows(p))) continue;
@@ -273,7 +271,7 @@ struct Write8 {
                                                       int group, int lane, const float *row) {
     const int w = lane % R::LPR, h = group * RPP + lane / R::LPR;
     RowLoad<T> weight;
-    if (NORM && !WHICH) weight.load(static_cast<const T *>(a.k_weight) + 8 * w, R::HALF);
+    if (NORM && !WHICH) weight = load_weights<T>(a.k_weight, w, R::HALF);
     LaneRow y;
     widen_row(in.raw, y);
     prepare<WHICH>(a, y, weight, w, row);

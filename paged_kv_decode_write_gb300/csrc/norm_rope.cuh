@@ -21,8 +21,6 @@
 namespace photon {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormMaxTile = 8;    // tokens of a CTA
-constexpr int kNormDivBits = 28;   // row / heads = row * div >> 28
 
 // A lane's 16 values of a row, as pairs of neighbouring dims for the packed fp32
 // instructions (two elements each): a: dims 8w .. 8w + 7, b: those + D/2.
@@ -112,33 +110,41 @@ __device__ __forceinline__ void rope_table_rows(float (*cs)[RopeRow<D>::STRIDE],
   }
 }
 
-// Rotates a lane's 8 pairs.  NEOX: (a, b) element by element; GPT-J: the
-// neighbours of a, then of b.  cs: the token's table row.
-template <int D>
-__device__ __forceinline__ void rotate_row(LaneRow &x, const float *cs, int w, bool gptj) {
-  using R = RopeRow<D>;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 t = *reinterpret_cast<const float4 *>(cs + 4 * (j * R::LPR + w));
-    if (gptj) {
-      float2 &p = j < 2 ? x.a[2 * j] : x.b[2 * j - 4], &q = j < 2 ? x.a[2 * j + 1] : x.b[2 * j - 3];
-      p = make_float2(fmaf(p.x, t.x, -(p.y * t.z)), fmaf(p.y, t.x, p.x * t.z));
-      q = make_float2(fmaf(q.x, t.y, -(q.y * t.w)), fmaf(q.y, t.y, q.x * t.w));
-    } else {
-      const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), u = x.a[j], v = x.b[j];
-      const float2 vs = __fmul2_rn(v, s);
-      x.a[j] = __ffma2_rn(u, c, make_float2(-vs.x, -vs.y));
-      x.b[j] = __ffma2_rn(v, c, __fmul2_rn(u, s));
-    }
+// Rotates a lane's 8 pairs, two per chunk of its token's row.  NEOX: (a, b) element by
+// element; GPT-J: the neighbours of a, then of b.
+__device__ __forceinline__ void rotate_chunk(LaneRow &x, int j, const float4 &t, bool gptj) {
+  if (gptj) {
+    float2 &p = j < 2 ? x.a[2 * j] : x.b[2 * j - 4], &q = j < 2 ? x.a[2 * j + 1] : x.b[2 * j - 3];
+    p = make_float2(fmaf(p.x, t.x, -(p.y * t.z)), fmaf(p.y, t.x, p.x * t.z));
+    q = make_float2(fmaf(q.x, t.y, -(q.y * t.w)), fmaf(q.y, t.y, q.x * t.w));
+  } else {
+    const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), u = x.a[j], v = x.b[j];
+    const float2 vs = __fmul2_rn(v, s);
+    x.a[j] = __ffma2_rn(u, c, make_float2(-vs.x, -vs.y));
+    x.b[j] = __ffma2_rn(v, c, __fmul2_rn(u, s));
   }
 }
+// A lane's chunks of a token's row.
+template <int D>
+struct RowAt {
+  const float *cs;
+  int w;
+  __device__ __forceinline__ float4 operator[](int j) const {
+    return *reinterpret_cast<const float4 *>(cs + 4 * (j * RopeRow<D>::LPR + w));
+  }
+};
+template <int D>
+__device__ __forceinline__ void rotate_row(LaneRow &x, const RowAt<D> &row, bool gptj) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) rotate_chunk(x, j, row[j], gptj);
+}
 
-// The lane's weights of a norm, as fp32.
+// The lane's weights of a norm.
 template <typename T>
-__device__ __forceinline__ void load_weights(const void *weight, int w, int half, LaneRow &out) {
+__device__ __forceinline__ RowLoad<T> load_weights(const void *weight, int w, int half) {
   RowLoad<T> r;
   r.load(static_cast<const T *>(weight) + 8 * w, half);
-  widen_row(r, out);
+  return r;
 }
 
 __device__ __forceinline__ void scale_row(LaneRow &x, const LaneRow &f) {
@@ -173,43 +179,74 @@ __device__ __forceinline__ float inv_rms(const LaneRow &x, float eps) {
   return rsqrtf(fmaf(a, 1.f / D, eps));
 }
 
-// Norm and rotation of a row: the sum's shuffles run beside the rotation of x w,
-// the factor comes last.  cs NULL: no rotation.
-template <int D>
-__device__ __forceinline__ void norm_rope_row(LaneRow &x, const LaneRow &weight, float eps, const float *cs, int w,
-                                              bool gptj) {
+// Norm and rotation (if asked for) of a row: the sum's shuffles run beside the
+// rotation of x w, the factor comes last.  The weights stay as they were loaded: the
+// registers of another fp32 row would cost a CTA per SM.
+template <typename T, int D>
+__device__ __forceinline__ void norm_rope_row(LaneRow &x, const RowLoad<T> &weight, float eps, bool rotate,
+                                              const RowAt<D> &row, bool gptj) {
   const float inv = inv_rms<D>(x, eps);
-  scale_row(x, weight);
-  if (cs) rotate_row<D>(x, cs, w, gptj);
+  LaneRow f;
+  widen_row(weight, f);
+  scale_row(x, f);
+  if (rotate) rotate_row(x, row, gptj);
   scale_row(x, inv);
 }
 
-// One tile of query rows, [tokens][heads][D] contiguous: normalised and rotated
-// in place, neighbouring rows of a token by neighbouring lanes.
+// The table row of one token, by its warp; scratch: STRIDE floats of the warp's own.
+template <int D>
+__device__ __forceinline__ void token_turns(float *scratch, int pos, const unsigned long long *turns, bool gptj) {
+  using R = RopeRow<D>;
+  for (int pair = threadIdx.x & 31; pair < R::HALF; pair += 32) {
+    const float2 v = cos_sin_of_turn(turn_of(pos, turns[pair]));
+    float *at = scratch + R::at(pair, gptj);
+    at[0] = v.x;
+    at[2] = v.y;
+  }
+  __syncwarp();
+}
+
+// A warp's share of a tile of tokens: of 8 tokens one each, of fewer a token's heads
+// in turn between 8 / tokens warps, so that no warp waits for another.
+struct TokenShare {
+  int64_t token;  // -1: none
+  int part, parts;
+  __device__ __forceinline__ TokenShare(int tile, int tile_log2, int tokens) {
+    const int warp = threadIdx.x >> 5, split = 3 - tile_log2;
+    const int64_t t = (static_cast<int64_t>(tile) << tile_log2) + (warp >> split);
+    token = t < tokens ? t : -1;
+    part = warp & ((1 << split) - 1);
+    parts = 1 << split;
+  }
+};
+
+// One tile of query tokens: every head normalised and rotated in place, neighbouring
+// heads of a token by neighbouring lanes, the next ones on their way.
 template <typename Tag, int D>
-__device__ __forceinline__ void norm_rope_q_tile(const NormRopeArgs &a, int tile, float (*cs)[RopeRow<D>::STRIDE]) {
+__device__ __forceinline__ void norm_rope_q_tile(const NormRopeArgs &a, int tile, float (*scratch)[RopeRow<D>::STRIDE]) {
   using T = typename Tag::T;
   using R = RopeRow<D>;
-  constexpr int STEP = kNormThreads / R::LPR;
-  const int t0 = tile << a.q_tile_log2, n = min(1 << a.q_tile_log2, a.num_q_tokens - t0);
-  const int rows = n * a.num_q_heads;
-  const int w = threadIdx.x % R::LPR, first = threadIdx.x / R::LPR;
+  constexpr int RPP = 32 / R::LPR;  // rows of a warp
+  const TokenShare mine(tile, a.q_tile_log2, a.num_q_tokens);
+  if (mine.token < 0) return;
+  const int lane = threadIdx.x & 31, w = lane % R::LPR, H = a.num_q_heads;
   const bool rotate = a.rope_style != PHOTON_ROPE_NONE, gptj = a.rope_style == PHOTON_ROPE_GPTJ;
-  T *base = static_cast<T *>(a.q) + static_cast<int64_t>(t0) * a.num_q_heads * D + 8 * w;
+  T *q = static_cast<T *>(a.q) + mine.token * H * D + 8 * w;
+  // heads past the last repeat it, for the shuffles
+  auto row = [&](int group) { return q + static_cast<int64_t>(min(group * RPP + lane / R::LPR, H - 1)) * D; };
+  const int groups = (H + RPP - 1) / RPP;
+  if (mine.part >= groups) return;
   RowLoad<T> next;
-  next.load(base + min(first, rows - 1) * D, R::HALF);
-  LaneRow weight;
-  load_weights<T>(a.q_weight, w, R::HALF, weight);
-  if (rotate) rope_table_rows<D>(cs, n, a.turns, gptj, [&](int t) { return a.q_positions[t0 + t]; });
-  __syncthreads();
-  for (int r0 = 0; r0 < rows; r0 += STEP) {  // lanes past the last row repeat it, for the shuffles
-    const int r = min(r0 + first, rows - 1);
+  next.load(row(mine.part), R::HALF);
+  const RowLoad<T> weight = load_weights<T>(a.q_weight, w, R::HALF);
+  const RowAt<D> turns{scratch[threadIdx.x >> 5], w};
+  if (rotate) token_turns<D>(scratch[threadIdx.x >> 5], a.q_positions[mine.token], a.turns, gptj);
+  for (int g = mine.part; g < groups; g += mine.parts) {
     LaneRow x;
     widen_row(next, x);
-    if (r0 + STEP < rows) next.load(base + min(r0 + STEP + first, rows - 1) * D, R::HALF);
-    norm_rope_row<D>(x, weight, a.eps, rotate ? cs[static_cast<uint32_t>(r) * a.q_div >> kNormDivBits] : nullptr, w,
-                     gptj);
-    if (r0 + first < rows) store_row(base + r * D, R::HALF, x);
+    if (g + mine.parts < groups) next.load(row(g + mine.parts), R::HALF);
+    norm_rope_row<T, D>(x, weight, a.eps, rotate, turns, gptj);
+    if (g * RPP + lane / R::LPR < H) store_row(row(g), R::HALF, x);
   }
 }
 

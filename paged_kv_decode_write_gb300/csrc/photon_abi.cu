@@ -738,7 +738,6 @@ int prepare_norm_write(void *q, const int32_t *q_positions, int32_t num_q_tokens
   if (num_q_tokens > 0) {
     if (num_q_heads <= 0 || !q || !q_positions || !q_weight) return PHOTON_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(q_weight, 16) || !aligned(q_positions, 4)) return PHOTON_ERR_INVALID_ARG;
-    if (num_q_heads > kNormMaxHeads) return PHOTON_ERR_UNSUPPORTED;
   }
   if (num_tokens > 0) {
     if (!k || !v || !positions || !slot_mapping || (norm && !k_weight)) return PHOTON_ERR_INVALID_ARG;
@@ -762,8 +761,6 @@ int prepare_norm_write(void *q, const int32_t *q_positions, int32_t num_q_tokens
   a->num_kv_heads = num_kv_heads;
   a->rope_style = rope_style;
   a->eps = eps;
-  a->q_div = num_q_heads > 0 ? ((1u << 28) + num_q_heads - 1) / num_q_heads : 0;
-  a->kv_div = ((1u << 28) + num_kv_heads - 1) / num_kv_heads;
   if (rotate && !*nothing) {
     double freq[kMaxRopePairs];
     frequencies(rope_theta, head_dim, freq);
@@ -812,7 +809,6 @@ int photon_qk_norm_rope_kv_cache_write(void *q, const int32_t *q_positions, int3
   if (num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PHOTON_ERR_INVALID_ARG;
   if (block_size != kBlockSize) return PHOTON_ERR_UNSUPPORTED;
   if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256) return PHOTON_ERR_UNSUPPORTED;
-  if (num_kv_heads > kNormMaxHeads) return PHOTON_ERR_UNSUPPORTED;
   if (num_blocks > INT64_MAX / (static_cast<int64_t>(num_kv_heads) * block_size * head_dim))
     return PHOTON_ERR_INVALID_ARG;
   photon::NormRopeArgs a{};

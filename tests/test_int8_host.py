@@ -93,15 +93,6 @@ def test_the_corrected_product_is_the_quotient_by_127():
         assert np.array_equal(_fma(_fma(q, -127.0, m), inv, q), m / _f(127))
 
 
-def test_row_divisions_are_exact():
-    """row * ceil(2^28 / heads) >> 28 is row / heads for the rows of 8 tokens."""
-    for heads in list(range(1, 70)) + [96, 127, 128, 1000, 1024, 4095, 4096]:
-        div = ((1 << 28) + heads - 1) // heads
-        r = np.arange(8 * heads, dtype=np.uint64)
-        assert int((r * np.uint64(div)).max()) < 2 ** 32
-        assert np.array_equal((r * np.uint64(div)) >> np.uint64(28), r // np.uint64(heads))
-
-
 def test_rotation_table_is_within_its_bound():
     """cos and sin of a fraction of a turn: the nearest quarter off exactly, the
     rest by Taylor series in fp32, within 2^-23 for fractions of every kind."""
@@ -167,10 +158,10 @@ def test_norm_writes_refuse_before_any_launch(L, pool):
         assert f(**kw) == -1, kw
     if not pool:
         assert f(vc=0) == -1 and f(vc=8) == -1
-        assert f(H=5000) == -2 and f(d=512) == -2
+        assert f(d=512) == -2
     else:
         assert f(d=32) == -2 and f(d=256) == -2 and f(H=1025) == -2 and f(nb=2 ** 31) == -2
-    assert f(bs=32) == -2 and f(d=96) == -2 and f(Hq=5000) == -2
+    assert f(bs=32) == -2 and f(d=96) == -2
     assert f(T=0, Tq=0, q=0, k=0) == 0
     assert f(T=0, Tq=0, style=2, theta=-1.0) == 0             # theta unused without rotation
 
