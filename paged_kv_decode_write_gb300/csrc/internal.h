@@ -84,7 +84,7 @@ struct NormRopeArgs {
   int32_t rope_style;
   float eps;
   unsigned long long turns[kMaxRopePairs];
-  int32_t q_tiles;  // CTAs that take query tiles (the first ones)
+  int32_t q_tiles;  // CTAs that take query tiles
   int32_t q_tile_log2;
   int32_t tile_log2;
 };
@@ -203,7 +203,8 @@ cudaError_t launch_kv_cache_write_fp4(const WriteArgs &a, photon_dtype in_dt, un
 cudaError_t launch_kv_cache_read_fp4(const CacheReadArgs &a, photon_dtype out_dt, unsigned int *err,
                                      cudaStream_t st);
 cudaError_t launch_decode_partial_fp4(const DecodeArgs &a, unsigned int *err, cudaStream_t st);
-cudaError_t launch_decode_merge_fp4(const DecodeArgs &a, cudaStream_t st);
+// Merge of the pieces that the 4-bit and the 8-bit decode leave.
+cudaError_t launch_decode_merge_pieces(const DecodeArgs &a, cudaStream_t st);
 // log2 of a CTA's tokens, at most `most`: as many as leave two CTAs per SM.
 int norm_tile_log2(int64_t tokens, int most);
 cudaError_t launch_qk_norm_rope_write(NormRopeArgs a, photon_dtype dt, int head_dim, unsigned int *err,

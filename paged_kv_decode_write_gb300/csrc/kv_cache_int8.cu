@@ -17,10 +17,17 @@
 // same step.)
 //
 // What a block's tokens share is the scale, so the unit of work is a run: the
-// tokens of one block, next to each other in the call.  A warp takes one run's K
-// or V of one head: 16 rows by offset, 16 values per lane and row in registers, one
-// reduction for m, then the codes, 8 bytes per store.  A CTA takes the runs that
-// begin in its tile of tokens, all heads, over one (cos, sin) table.
+// tokens of one block, next to each other in the call.  A warp takes one run's K or
+// V of one head, 16 rows by offset, with one reduction for m; of runs of one token,
+// several heads at once.  A CTA walks tiles of tokens and takes the runs that begin in
+// them, all heads, over one (cos, sin) table per tile.
+//
+// What bounds it: the arithmetic's issue and latency at 16 (d 64) or 8 (d 128) warps per
+// SM, not memory: 16384 tokens of 8 x 64, bf16, take 17.0 us for 50 MB (7.4 at the copy rate),
+// 13.8 without the rotation, and without either loads or stores still 12.9; 65536 tokens
+// 54.6 us, 0.54 of the copy rate; 8192 of 8 x 128 18.4 us; 64 tokens of a decode step 3.9 us,
+// two dependent loads and a launch.  The read is bound by DRAM, two thirds of it
+// writes: 32768 tokens of 8 x 128 34.2 us, 0.87 of the copy rate.
 #include <climits>
 
 #include "int8.cuh"
@@ -295,16 +302,13 @@ struct Write8 {
 };
 
 // CTAs per SM that the write's registers allow.
-template <typename T, int D>
-constexpr int int8_write_ctas() {
-  return D == 64 ? 2 : 1;
-}
+constexpr int int8_write_ctas(int head_dim) { return head_dim == 64 ? 2 : 1; }
 
 // The first kv_ctas CTAs walk the tiles of tokens, the others take a query tile
 // each.  A tile's slots and positions are loaded one tile ahead, a unit's rows and
 // scale one unit ahead, across runs and tiles.
 template <typename Tag, int D, bool NORM>
-__global__ void __launch_bounds__(kNormThreads, int8_write_ctas<typename Tag::T, D>())
+__global__ void __launch_bounds__(kNormThreads, int8_write_ctas(D))
     kv_cache_write_int8_kernel(const __grid_constant__ NormRopeArgs a, int kv_ctas, int tiles, unsigned int *err) {
   using R = RopeRow<D>;
   using W = Write8<Tag, D, NORM>;
@@ -539,11 +543,12 @@ cudaError_t launch_read(const CacheReadArgs &a, unsigned int *err, cudaStream_t 
 
 template <typename Tag, int D>
 cudaError_t launch_write(NormRopeArgs a, bool norm, unsigned int *err, cudaStream_t st) {
-  const int64_t room0 = static_cast<int64_t>(device_sm_count()) * int8_write_ctas<typename Tag::T, D>();
+  // tokens per tile: as few as give every resident CTA one tile, up to 16 (777 fp32 tokens of
+  // 4 x 128: 5.5 us, 8.6 with a quarter of them in a tile, three tiles to a CTA)
+  const int64_t room = static_cast<int64_t>(device_sm_count()) * int8_write_ctas(D);
   a.tile_log2 = 0;
-  while ((1 << a.tile_log2) < kInt8MaxTile && (static_cast<int64_t>(a.num_tokens) >> a.tile_log2) > room0) ++a.tile_log2;
+  while ((1 << a.tile_log2) < kInt8MaxTile && (static_cast<int64_t>(a.num_tokens) >> a.tile_log2) > room) ++a.tile_log2;
   const int64_t tiles = (static_cast<int64_t>(a.num_tokens) + (1 << a.tile_log2) - 1) >> a.tile_log2;
-  const int64_t room = static_cast<int64_t>(device_sm_count()) * int8_write_ctas<typename Tag::T, D>();
   const int64_t kv_ctas = tiles < room ? tiles : room, ctas = kv_ctas + a.q_tiles;
   if (ctas == 0) return cudaSuccess;
   if (ctas > INT32_MAX || tiles + kv_ctas > INT32_MAX) return cudaErrorInvalidValue;
@@ -555,13 +560,14 @@ cudaError_t launch_write(NormRopeArgs a, bool norm, unsigned int *err, cudaStrea
 }  // namespace
 
 // Query rows from which they get a launch of their own, in the bf16 / fp32 write's
-// kernel: this one's registers leave 8 or 16 warps per SM, that one's 32.  262144 rows of d
-// 128 with 16384 tokens: 90.9 -> 71.5 us; 131072 of d 64 with 4096 tokens 10.9 against 14.2.
-constexpr int64_t kQueryRowsApart = 262144;
+// kernel, whose registers leave 32 warps per SM to this one's 16 (d 64) or 8 (d 128).  d 64:
+// 524288 rows, with 16384 tokens, 45.5 -> 44.0 us, 262144 24.9 against 25.7; d 128: 131072 rows,
+// with 8192 tokens, 44.7 -> 38.3, 65536 18.6 against 20.2.
+constexpr int64_t query_rows_apart(int head_dim) { return head_dim == 64 ? 524288 : 131072; }
 
 cudaError_t launch_kv_cache_write_int8(NormRopeArgs a, bool norm, photon_dtype in_dt, int head_dim,
                                        unsigned int *err, cudaStream_t st) {
-  if (static_cast<int64_t>(a.num_q_tokens) * a.num_q_heads >= kQueryRowsApart) {
+  if (static_cast<int64_t>(a.num_q_tokens) * a.num_q_heads >= query_rows_apart(head_dim)) {
     NormRopeArgs q = a;
     q.num_tokens = 0;
     const cudaError_t e = launch_qk_norm_rope_write(q, in_dt, head_dim, err, st);

@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(STREAMS * D / 4) fp4_merge_kernel(const Decode
 
 }  // namespace
 
-cudaError_t launch_decode_merge_fp4(const DecodeArgs &a, cudaStream_t st) {
+cudaError_t launch_decode_merge_pieces(const DecodeArgs &a, cudaStream_t st) {
   if (!balanced_pieces(a)) return launch_decode_reduce(a, st);  // fixed partitions
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   if (rows > INT32_MAX) return cudaErrorInvalidValue;

@@ -25,6 +25,13 @@
 //    the largest; the accumulators carry 2^(14 - E) to the end of the item, the sum
 //    never.  For an fp32 output the remainder of that rounding follows in a second
 //    MMA (SPLIT).  Sums, maxima and accumulators are fp32.
+//
+// What bounds it: DRAM on long steps (with the merge, 128 contexts of up to 32k tokens,
+// d 64, 2.15 GB: 313 us, 6.87 TB/s where a copy reads and writes 6.79; 64 of up to 16k, d 128, 161
+// us, 0.99 of the copy rate); between, start-up, uneven ends and the merge (64 ragged
+// sequences of d 128, 258 MB: 46.5 us, 0.82: the first page lands after 3 to 4 us, the bulk runs
+// at the copy rate, the last warp ends 4 us after the median one, the merge takes 1.5);
+// latency on short ones (one context of 1024: 3.9 us).
 #include <algorithm>
 #include <atomic>
 

@@ -215,7 +215,7 @@ def test_many_queries_beside_the_write():
     torch = _torch()
     pk = ensure_built()
     gen = torch.Generator(device="cuda").manual_seed(3)
-    T, H, Hq, d, nb = 8200, 2, 32, 64, 520
+    T, H, Hq, d, nb = 8200, 2, 16, 128, 520
     mk = lambda h: torch.randn(T, h, d, generator=gen, device="cuda").bfloat16()
     q, k, v = mk(Hq), mk(H), mk(H)
     wq, wk = (1 + 0.2 * torch.randn(d, generator=gen, device="cuda") for _ in range(2))
