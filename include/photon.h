@@ -529,7 +529,8 @@ int photon_kv_cache_write_int8(const void *k, const void *v, const int32_t *posi
  * photon_qk_norm_rope_kv_cache_write_int8 -- photon_qk_norm_rope_kv_cache_write
  * into an 8-bit pool: y = RoPE(N(k, k_weight)) in fp32, quantised as
  * photon_kv_cache_write_int8 does, and q normalised and rotated in place
- * (in_dtype), in one launch.
+ * (in_dtype), in one launch (two where the query rows are very many: from 131072
+ * at head_dim 128, 524288 at 64).
  */
 int photon_qk_norm_rope_kv_cache_write_int8(void *q, const int32_t *q_positions, int32_t num_q_tokens,
                                             int32_t num_q_heads, const void *k, const void *v,
