@@ -556,9 +556,10 @@ int photon_kv_cache_read_int8(const void *kv_cache, const int64_t *slot_mapping,
  * photon_paged_attention_decode_int8 -- photon_paged_attention_decode over an
  * 8-bit pool: the same attention on the dequantised values.  q is bf16 (already
  * rotated) of any magnitude.  The scores, softmax and sums are fp32; a softmax
- * weight times its block's V scale enters the second product in f16 (11
- * significant bits) for a bf16 output, as f16 and its f16 remainder (22) for an
- * fp32 one, scaled by the largest V scale so far.  K and V may have any magnitude
+ * weight times its block's V scale enters the second product as f16 and its f16
+ * remainder: within 2^-22 of itself, or 2^-33 of the largest weight times the
+ * largest V scale of the context so far where that is more.  out_dtype decides the
+ * last rounding and nothing else.  K and V may have any magnitude
  * whose sums fit fp32: |k| below 2^110, |v| summed over a context below 2^127,
  * |scale| times a row's largest |q| below 2^110, and the scores themselves.
  * Workspace as for photon_paged_attention_decode; the split-K pieces are

@@ -21,17 +21,19 @@
 //  * Weights and their sum are kept relative to 2^m, m at most 2^6 above the
 //    largest score so far.  The weights of the second product take s_V 2^(14 - E),
 //    E the largest exponent of the item's s_V so far: below 2^15 whatever the
-//    values' magnitude, rounded to f16 with relative error 2^-12 down to 2^-22 of
-//    the largest; the accumulators carry 2^(14 - E) to the end of the item, the sum
-//    never.  For an fp32 output the remainder of that rounding follows in a second
-//    MMA (SPLIT).  Sums, maxima and accumulators are fp32.
+//    values' magnitude.  They enter as their f16 rounding and, in a second MMA, the
+//    f16 remainder: within 2^-22 of themselves or 2^-25, and the largest is 2^8 or more.
+//    (f16 alone, 2^-11, put 8 to 10 % of bf16 outputs on the other side of a rounding
+//    border; the second MMA costs 1 % of ragged batches of d 128, 3 % of long steps of
+//    d 64.)  The accumulators carry 2^(14 - E) to the end of the item, the sum never.
+//    Sums, maxima and accumulators are fp32.
 //
 // What bounds it: DRAM on long steps (with the merge, 128 contexts of up to 32k tokens,
-// d 64, 2.15 GB: 313 us, 6.87 TB/s where a copy reads and writes 6.79; 64 of up to 16k, d 128, 161
-// us, 0.99 of the copy rate); between, start-up, uneven ends and the merge (64 ragged
-// sequences of d 128, 258 MB: 46.5 us, 0.82: the first page lands after 3 to 4 us, the bulk runs
+// d 64, 2.15 GB: 329 us, 6.55 TB/s where a copy reads and writes 6.79; 64 of up to 16k, d 128, 164
+// us, 0.97 of the copy rate); between, start-up, uneven ends and the merge (64 ragged
+// sequences of d 128, 258 MB: 47.5 us, 0.80: the first page lands after 3 to 4 us, the bulk runs
 // at the copy rate, the last warp ends 4 us after the median one, the merge takes 1.5);
-// latency on short ones (one context of 1024: 3.9 us).
+// latency on short ones (one context of 1024: 4.1 us).
 #include <algorithm>
 #include <atomic>
 
@@ -114,7 +116,7 @@ __device__ __forceinline__ float load_cluster(const float *p, uint32_t rank) {
   return v;
 }
 
-template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, Mode MODE>
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, Mode MODE>
 __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
     paged_decode_int8_kernel(const DecodeArgs a, unsigned int *err) {
   using R = Int8Ring<D, PP, ST, NW>;
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
             }
         }
         const float down = pow2(14 - E);
-        uint32_t ph[PP][2], pl[SPLIT ? PP : 1][2];
+        uint32_t ph[PP][2], pl[PP][2];
 #pragma unroll
         for (int i = 0; i < PP; ++i) {
           const float s = sv[i] * down;
@@ -384,10 +386,8 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
             const float w0 = p0 * s, w1 = p1 * s;
             const uint32_t h = pack_half2(w0, w1);
             ph[i][n] = transpose_8x8(h);
-            if constexpr (SPLIT) {
-              const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-              pl[i][n] = transpose_8x8(pack_half2(w0 - r.x, w1 - r.y));
-            }
+            const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            pl[i][n] = transpose_8x8(pack_half2(w0 - r.x, w1 - r.y));
           }
         }
         // ---- O^T += V^T P^T: bytes of the same dim of two tokens make an f16 pair of the A operand
@@ -398,18 +398,20 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
             const unsigned char *vp = stage + i * REC + 16 * D + 1024 * hh + 16 * lane;
             const uint4 v0 = *reinterpret_cast<const uint4 *>(vp);        // tokens 4c, 4c + 1
             const uint4 v1 = *reinterpret_cast<const uint4 *>(vp + 512);  // tokens 4c + 2, 4c + 3
-            auto tile = [&](float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-              mma_f16(acc, a0, a1, a2, a3, ph[i][0], ph[i][1]);
-              if constexpr (SPLIT) mma_f16(acc, a0, a1, a2, a3, pl[i][0], pl[i][1]);
-            };
-            tile(o[hh][0], codes_across<0>(v0.x, v0.z), codes_across<1>(v0.x, v0.z),
-                 codes_across<0>(v1.x, v1.z), codes_across<1>(v1.x, v1.z));
-            tile(o[hh][1], codes_across<2>(v0.x, v0.z), codes_across<3>(v0.x, v0.z),
-                 codes_across<2>(v1.x, v1.z), codes_across<3>(v1.x, v1.z));
-            tile(o[hh][2], codes_across<0>(v0.y, v0.w), codes_across<1>(v0.y, v0.w),
-                 codes_across<0>(v1.y, v1.w), codes_across<1>(v1.y, v1.w));
-            tile(o[hh][3], codes_across<2>(v0.y, v0.w), codes_across<3>(v0.y, v0.w),
-                 codes_across<2>(v1.y, v1.w), codes_across<3>(v1.y, v1.w));
+            // the four weights' MMAs, then the four remainders': none waits for the one before
+            uint32_t w[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t x0 = t < 2 ? v0.x : v0.y, y0 = t < 2 ? v0.z : v0.w;
+              const uint32_t x1 = t < 2 ? v1.x : v1.y, y1 = t < 2 ? v1.z : v1.w;
+              w[t][0] = t & 1 ? codes_across<2>(x0, y0) : codes_across<0>(x0, y0);
+              w[t][1] = t & 1 ? codes_across<3>(x0, y0) : codes_across<1>(x0, y0);
+              w[t][2] = t & 1 ? codes_across<2>(x1, y1) : codes_across<0>(x1, y1);
+              w[t][3] = t & 1 ? codes_across<3>(x1, y1) : codes_across<1>(x1, y1);
+              mma_f16(o[hh][t], w[t][0], w[t][1], w[t][2], w[t][3], ph[i][0], ph[i][1]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) mma_f16(o[hh][t], w[t][0], w[t][1], w[t][2], w[t][3], pl[i][0], pl[i][1]);
           }
       }
       __syncwarp();  // the stage is read before the next copies overwrite it
@@ -615,11 +617,11 @@ inline bool team_step(const DecodeArgs &a, int64_t items, int64_t ctas, int warp
 
 enum class Int8Fit { kAlways, kLongSteps, kTeams };  // when launch_int8_kern takes a step
 
-template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, bool SPLIT, Int8Fit FIT>
+template <int D, int PP, int ST, int NW, int MIN_CTAS, bool BAL, Int8Fit FIT>
 cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
   constexpr bool TEAM = FIT == Int8Fit::kTeams;
   constexpr int SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
-  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, SPLIT, TEAM ? Mode::kTeams : Mode::kWarps>;
+  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, BAL, TEAM ? Mode::kTeams : Mode::kWarps>;
   static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -661,10 +663,11 @@ cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_
 // up to 16384, 16 pages: 10.5 against 9.3; one of 8192, d 128, 8 pages: 9.4 against 8.4).
 constexpr int kClusterMax = 8, kClusterPages = 16, kClusterFewBytes = 16384;
 
-template <int D, int PP, int NW, bool SPLIT>
+template <int D, int PP, int NW>
 cudaError_t launch_int8_cluster(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
   constexpr int ST = 2, SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
-  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, 1, false, SPLIT, Mode::kCluster>;
+  constexpr int MIN_CTAS = PP == 1 ? 4 : 1;
+  auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, false, Mode::kCluster>;
   static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -705,44 +708,43 @@ cudaError_t launch_int8_cluster(const DecodeArgs &a, unsigned int *err, cudaStre
 // The cluster's width: 8 warps per CTA while the pairs of sequence and KV head are few,
 // so that a pair finds as many warps as possible; 4 where whole contexts per CTA fill
 // the GPU (d 64, 512 pairs of 600 tokens: 9.7 us, 12.8 with 8 warps); in d 128 steps of one
-// page and so three CTAs per SM for yet more pairs (512 pairs of 600 tokens: 16.3, 18.9 with two).
-template <int D, bool SPLIT>
+// page and so four CTAs per SM for yet more pairs (512 pairs of 600 tokens: 17.0, 19.5 with steps of
+// two; with the registers of three CTAs 21.4, but 64 ragged contexts of up to 1000 20.4 against 21.4).
+template <int D>
 cudaError_t launch_int8_clusters(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *taken) {
   const int64_t sms = device_sm_count(), pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   if constexpr (D == 64) {
-    return pairs <= 3 * sms ? launch_int8_cluster<D, 2, 8, SPLIT>(a, err, stream, taken)
-                            : launch_int8_cluster<D, 2, 4, SPLIT>(a, err, stream, taken);
+    return pairs <= 3 * sms ? launch_int8_cluster<D, 2, 8>(a, err, stream, taken)
+                            : launch_int8_cluster<D, 2, 4>(a, err, stream, taken);
   } else {
-    return pairs <= sms       ? launch_int8_cluster<D, 2, 8, SPLIT>(a, err, stream, taken)
-           : pairs <= 3 * sms ? launch_int8_cluster<D, 2, 4, SPLIT>(a, err, stream, taken)
-                              : launch_int8_cluster<D, 1, 4, SPLIT>(a, err, stream, taken);
+    return pairs <= sms       ? launch_int8_cluster<D, 2, 8>(a, err, stream, taken)
+           : pairs <= 3 * sms ? launch_int8_cluster<D, 2, 4>(a, err, stream, taken)
+                              : launch_int8_cluster<D, 1, 4>(a, err, stream, taken);
   }
 }
 
 // *whole: every row is written, nothing to merge.
-template <int D, bool BAL, bool SPLIT>
+template <int D, bool BAL>
 cudaError_t launch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t stream, bool *whole) {
-  cudaError_t e = launch_int8_clusters<D, SPLIT>(a, err, stream, whole);
+  cudaError_t e = launch_int8_clusters<D>(a, err, stream, whole);
   if (e != cudaSuccess || *whole) return e;
   bool taken = false;
-  e = launch_int8_kern<D, 2, 2, 4, 1, BAL, SPLIT, Int8Fit::kTeams>(a, err, stream, &taken);
+  e = launch_int8_kern<D, 2, 2, 4, 1, BAL, Int8Fit::kTeams>(a, err, stream, &taken);
   if (e != cudaSuccess || taken) return e;
   if constexpr (D == 64) {
     if constexpr (BAL) {
-      e = launch_int8_kern<D, 2, 2, 12, 1, true, SPLIT, Int8Fit::kLongSteps>(a, err, stream, &taken);
+      e = launch_int8_kern<D, 2, 2, 12, 1, true, Int8Fit::kLongSteps>(a, err, stream, &taken);
       if (e != cudaSuccess || taken) return e;
     }
-    return launch_int8_kern<D, 2, 2, 4, 4, BAL, SPLIT, Int8Fit::kAlways>(a, err, stream, &taken);
+    return launch_int8_kern<D, 2, 2, 4, 4, BAL, Int8Fit::kAlways>(a, err, stream, &taken);
   } else {
-    return launch_int8_kern<D, 2, 2, 8, 1, BAL, SPLIT, Int8Fit::kAlways>(a, err, stream, &taken);
+    return launch_int8_kern<D, 2, 2, 8, 1, BAL, Int8Fit::kAlways>(a, err, stream, &taken);
   }
 }
 
 template <int D>
 cudaError_t dispatch_int8(const DecodeArgs &a, unsigned int *err, cudaStream_t st, bool *whole) {
-  if (balanced_pieces(a))
-    return a.out_bf16 ? launch_int8<D, true, false>(a, err, st, whole) : launch_int8<D, true, true>(a, err, st, whole);
-  return a.out_bf16 ? launch_int8<D, false, false>(a, err, st, whole) : launch_int8<D, false, true>(a, err, st, whole);
+  return balanced_pieces(a) ? launch_int8<D, true>(a, err, st, whole) : launch_int8<D, false>(a, err, st, whole);
 }
 
 }  // namespace
