@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
       qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 2));
       int e = static_cast<int>(__float_as_uint(qm) >> 23) - 127;
       if (e == 128 || qm == 0.f) e = 0;
-      e = max(e, -100);
+      e = max(e, -126);  // 2^-e and 2^e are normal numbers; a subnormal row becomes at least 2^-7
       const float down = e == 127 ? 0x1p-127f : pow2(-e);  // 2^-e
       const float s = a.scale_log2 * pow2(e);
       sl[0] = __shfl_sync(0xffffffffu, s, 8 * c);
@@ -313,11 +313,11 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
           }
         }
         const float2 sc = *reinterpret_cast<const float2 *>(stage + i * REC + int8_scale_byte(D, 0));
-        const float f0 = sl[0] * sc.x, f1 = sl[1] * sc.x;
-        x[i][0] = acc[0] * f0;
-        x[i][1] = acc[1] * f1;
-        x[i][2] = acc[2] * f0;
-        x[i][3] = acc[3] * f1;
+        // K's scale first: |k| times a q below 2 stays in range, both factors together may not
+        x[i][0] = acc[0] * sc.x * sl[0];
+        x[i][1] = acc[1] * sc.x * sl[1];
+        x[i][2] = acc[2] * sc.x * sl[0];
+        x[i][3] = acc[3] * sc.x * sl[1];
         sv[i] = sc.y;
       }
       const int tok0 = (w.pg0 + w.page) * kBlockSize;

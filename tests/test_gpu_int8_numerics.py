@@ -50,3 +50,67 @@ def test_bf16_outputs_are_off_by_half_a_step_of_their_own(d, declared):
     kd, vd = int8.dequant(pool, d)
     fp32 = _tolerance(oracle.to_f64(q), kd, vd, ctx, 0.0, False, ref)
     assert (np.abs(got - ref) <= 0.5 * bf16_spacing(ref) + fp32).all()
+
+
+def _set_k_scales(pool, factor):
+    sc = int8.scales(pool).copy()
+    sc[..., 0] = (sc[..., 0] / sc[..., 0].max() * factor).astype(np.float32)
+    pool[:, :, -16:-8] = sc.view(np.uint8)
+
+
+@pytest.mark.parametrize("declared", DECLARED)
+@pytest.mark.parametrize("qexp,scale", [(-118, 2.0 ** 12), (-126, 2.0 ** 20), (-131, 2.0 ** 25)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tiny_queries_against_large_keys(qexp, scale, d, declared):
+    """q down to bf16's subnormal numbers, |k| up to 2^108, scores of order 10: a
+    row's largest value keeps its 8 bits whatever its exponent."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(-qexp)
+    ctx, H, G = [40, 300, 5], 2, 4
+    nb = 30
+    pool = _random_pool(rng, nb, H, d)
+    _set_k_scales(pool, 2.0 ** 101)
+    bt = _tables(rng, ctx, nb)
+    q, qt = _storage(rng.standard_normal((3, H * G, d)) * 2.0 ** qexp, "bf16")
+    got = _decode(pk, qt, _dev(pool), bt, ctx, scale, torch.float32, 64, max_ctx=declared).double().cpu().numpy()
+    ref = int8.paged_attention(q, pool, bt, ctx, scale)
+    kd, vd = int8.dequant(pool, d)
+    assert (np.abs(got - ref) <= _tolerance(oracle.to_f64(q), kd, vd, ctx, scale, False, ref)).all()
+
+
+@pytest.mark.parametrize("declared", DECLARED)
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_zero_stay_zero_whatever_the_factors(d, declared):
+    """Keys exactly orthogonal to a query have score 0 although the softmax scale,
+    |q| and the K scale together pass fp32's range; one token whose score does fit
+    takes the whole weight."""
+    torch = _torch()
+    pk = ensure_built()
+    rng = np.random.default_rng(d)
+    ctx, H, G, nb = [50, 200], 1, 4, 20
+    pool = _random_pool(rng, nb, H, d)
+    byte = int8.record_positions(d)[0]
+    pool[:, :, byte[:, ::2]] = 128                         # K is 0 in the even dims
+    _set_k_scales(pool, 2.0 ** 102)
+    bt = _tables(rng, ctx, nb)
+    x = rng.uniform(0.5, 1, (2, H * G, d)) * 2.0 ** 60
+    x[..., 1::2] = 0
+    q, qt = _storage(x, "bf16")
+    got = _decode(pk, qt, _dev(pool), bt, ctx, 2.0 ** 49, torch.float32, 64, max_ctx=declared).double().cpu().numpy()
+    ref = int8.paged_attention(q, pool, bt, ctx, 2.0 ** 49)
+    kd, vd = int8.dequant(pool, d)
+    V = np.abs(vd).max()
+    # the weights are exactly alike: the sums' roundings and the weights' 2^-22
+    assert (np.abs(got - ref) <= V * 2 * ((max(ctx) / 16 + 8) * 2.0 ** -23 + 2.0 ** -22)).all()
+    # 2^40 in dim 1 of q, 2^-19 of the largest (exact in f16), meets a code of 1 in token 33 of each
+    # context and zeros elsewhere: a score of some 2^120 there, 2^139 times the token's code before
+    x[..., 1] = 2.0 ** 40
+    q, qt = _storage(x, "bf16")
+    pool[:, :, byte[:, 1]] = 128
+    for s in range(2):
+        pool[bt[s, 2], :, byte[1, 1]] = 129
+    got = _decode(pk, qt, _dev(pool), bt, ctx, 2.0 ** -22, torch.float32, 64, max_ctx=declared).double().cpu().numpy()
+    _, vd = int8.dequant(pool, d)
+    want = np.stack([vd[bt[s, 2], :, 1] for s in range(2)])                         # [2, H, d]
+    assert (np.abs(got - want) <= np.abs(want) * 2.0 ** -20).all()
