@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
       qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 2));
       int e = static_cast<int>(__float_as_uint(qm) >> 23) - 127;
       if (e == 128 || qm == 0.f) e = 0;
-      e = max(e, -100);
+      e = max(e, -126);  // 2^-e and 2^e are normal numbers; a subnormal row becomes at least 2^-7
       float down = __uint_as_float(static_cast<uint32_t>(127 - min(e, 126)) << 23);  // 2^-e
       if (e == 127) down = 0x1p-127f;
       float s = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
