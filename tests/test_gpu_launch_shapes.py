@@ -7,6 +7,7 @@ import subprocess
 import numpy as np
 import pytest
 
+from tests import test_gpu_int8
 from tests.helpers import ensure_built
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +80,57 @@ def test_tiles_of_the_8_bit_write(d, per_sm):
         assert ctas == min(room, -(-T // tile)), T
 
 
+def _decode_launches(pk, B, H, G, d, max_ctx, part, out):
+    torch = _torch()
+    W = -(-max(max_ctx, 1) // 16)
+    n = pk.photon_paged_attention_workspace_size(B, H * G, d, max_ctx, part)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    q = torch.zeros(B, H * G, d, dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros(B, H * G, d, dtype=out, device="cuda")
+    pool = torch.zeros(1, H, 32 * d + 16, dtype=torch.uint8, device="cuda")
+    bt, cl = (torch.zeros(*s, dtype=torch.int32, device="cuda") for s in ((B, W), (B,)))
+    call = lambda st: pk.photon_paged_attention_decode_int8(q, pool, bt, cl, 0.1, o, max_ctx, part, ws, stream=st)
+    call(None)                                                     # sets the kernels' attributes up
+    return launches(call)
+
+
+# Whole contexts as items, too many for clusters: one piece per row and no merge.
+WHOLE_ITEMS = [(320, 1, 4500, 8, 1, 64, 8192, "f32"), (320, 1, 4500, 8, 2, 128, 8192, "bf16"), (64, 1, 6000, 8, 1, 128, 8192, "f32")]
+
+
+@pytest.mark.parametrize("B,lo,hi,H,G,d,part,out", WHOLE_ITEMS)
+def test_whole_contexts_as_items(B, lo, hi, H, G, d, part, out):
+    test_gpu_int8.test_decode_grids(B, lo, hi, H, G, d, part, out)
+
+
+def test_every_launch_shape_of_the_8_bit_decode_is_tested():
+    """The batches of test_decode_grids and of WHOLE_ITEMS, and the small ones declared as
+    they are and as long, take between them every kernel that the launcher can choose:
+    (head_dim, pages of a step, warps of a CTA, pieces by the page stream, how a CTA's warps share items)."""
+    torch = _torch()
+    pk = ensure_built()
+    parameters = lambda test: [m.args[1] for m in test.pytestmark if m.name == "parametrize"]
+    batches = []
+    for B, lo, hi, H, G, d, part, out in parameters(test_gpu_int8.test_decode_grids)[0] + WHOLE_ITEMS:
+        ctx = np.random.default_rng(B + hi).integers(lo, hi + 1, B)
+        if B > 2:
+            ctx[B // 2], ctx[B // 3] = 0, 1
+        batches.append((B, H, G, d, int(max(ctx.max(), 1)), part))
+    for ctx, part in test_gpu_int8.CONTEXTS:
+        for H, G in parameters(test_gpu_int8.test_decode_matches_the_oracle)[2]:
+            for declared in test_gpu_int8.DECLARED:
+                batches += [(len(ctx), H, G, d, declared or max(ctx), part) for d in (64, 128)]
+    seen = set()
+    for batch in batches:
+        for out in (torch.bfloat16, torch.float32):
+            first, *rest = _decode_launches(pk, *batch, out)
+            m = re.fullmatch(r"paged_decode_int8_kernel<(\d+), (\d+), 2, (\d+), \d, (true|false), \(Mode\)(\d)>", first[0])
+            d, pages, warps, pieces, mode = (int(x) if x.isdigit() else x == "true" for x in m.groups())
+            seen.add((d, pages, warps, pieces, ("warps", "team", "cluster")[mode]))
+            # pieces are merged by a second launch, whole rows by none
+            assert [n[0].split("<")[0] for n in rest] == (["fp4_merge_kernel"] if pieces else [])
+    assert seen == {(64, 2, 8, False, "cluster"), (64, 2, 4, False, "cluster"), (128, 2, 8, False, "cluster"),
+                    (128, 2, 4, False, "cluster"), (128, 1, 4, False, "cluster"),
+                    (64, 2, 4, True, "team"), (64, 2, 4, False, "team"), (128, 2, 4, True, "team"), (128, 2, 4, False, "team"),
+                    (64, 2, 12, True, "warps"), (64, 2, 4, True, "warps"), (64, 2, 4, False, "warps"), (128, 2, 8, True, "warps"),
+                    (128, 2, 8, False, "warps")}
