@@ -87,6 +87,7 @@ typedef enum {
 #define PHOTON_DEVERR_CONTEXT_RANGE 0x4u /* a context length above max_context_len or the table width: clamped */
 #define PHOTON_DEVERR_WAIT_TIMEOUT 0x8u  /* a bounded wait on a page copy gave up: item abandoned */
 #define PHOTON_DEVERR_METADATA 0x10u     /* photon_build_step_metadata_device refused a step (totals[3]) */
+#define PHOTON_DEVERR_BLOCK_ORDER 0x20u  /* an 8-bit write's tokens of one block do not stand together */
 
 /* Human-readable name of a status value (static string, never NULL). */
 const char *photon_status_string(int status);
@@ -512,9 +513,11 @@ size_t photon_kv_cache_int8_record_bytes(int32_t head_dim);
  *   k, v      device [num_tokens][num_kv_heads][head_dim], in_dtype (f32 or bf16), 16-B aligned
  *   kv_cache  device 8-bit pool, 16-B aligned
  *   slot_mapping  distinct slots; the tokens of one block stand next to each
- *             other, in any order, with nothing in between (lists by sequence and
- *             position do).  Where they do not, the blocks concerned hold no
- *             defined values
+ *             other, in any order, with nothing in between, a skipped token neither (lists
+ *             by sequence and position do).  Where they do not, the blocks concerned hold
+ *             no defined values; that sets PHOTON_DEVERR_BLOCK_ORDER in calls of at
+ *             most 256 tokens, and in longer ones where at most 15 tokens lie between a
+ *             block's tokens (farther apart it is not noticed)
  * head_dim 64 or 128, num_kv_heads <= 1024, num_blocks < 2^31
  * (PHOTON_ERR_UNSUPPORTED otherwise; the same for the calls below).  Other
  * arguments and errors as photon_kv_cache_write.

@@ -19,7 +19,7 @@ import numpy as np
 __all__ = [
     "PhotonError", "F32", "BF16", "ROPE_NEOX", "ROPE_GPTJ", "ROPE_NONE",
     "DEVERR_SLOT_RANGE", "DEVERR_BLOCK_RANGE", "DEVERR_CONTEXT_RANGE", "DEVERR_WAIT_TIMEOUT",
-    "DEVERR_METADATA",
+    "DEVERR_METADATA", "DEVERR_BLOCK_ORDER",
     "lib", "lib_path", "photon_version", "photon_status_string",
     "photon_kv_cache_write", "photon_rope_q_kv_cache_write", "photon_kv_cache_write_fp8",
     "photon_paged_attention_decode_fp8", "photon_paged_attention_partial_fp8",
@@ -40,7 +40,7 @@ __all__ = [
 F32, BF16 = 0, 1
 ROPE_NEOX, ROPE_GPTJ, ROPE_NONE = 0, 1, 2
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_RANGE, DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
-DEVERR_METADATA = 16
+DEVERR_METADATA, DEVERR_BLOCK_ORDER = 16, 32
 _ROPE = {"neox": ROPE_NEOX, "gptj": ROPE_GPTJ, "none": ROPE_NONE}
 STATIC_SCRATCH_BYTES = 32 * 1024 * 1024  # PHOTON_STATIC_SCRATCH_BYTES
 

@@ -22,6 +22,9 @@
 // several heads at once.  A CTA walks tiles of tokens and takes the runs that begin in
 // them, all heads, over one (cos, sin) table per tile.
 //
+// Two runs of one block in a call would race for its scale. Nothing orders them; where a
+// tile's 32 tokens, or those of a call of at most 256, show them, an error bit does.
+//
 // What bounds it: the arithmetic's issue and latency at 16 (d 64) or 8 (d 128) warps per
 // SM, not memory: 16384 tokens of 8 x 64, bf16, take 17.0 us for 50 MB (7.4 at the copy rate),
 // 13.8 without the rotation, and without either loads or stores still 12.9; 65536 tokens
@@ -392,6 +395,10 @@ __global__ void __launch_bounds__(kNormThreads, int8_write_ctas(D))
       off = static_cast<int>(slot) & (kBlockSize - 1);
       const int before = __shfl_up_sync(0xffffffffu, block, 1);
       const bool same = lane > 0 && live && before == block;
+      if (warp == 0) {  // a block's second run in the window
+        const uint32_t alike = __match_any_sync(0xffffffffu, block);
+        if (live && !same && (alike & ((1u << lane) - 1))) atomicOr(err, PHOTON_DEVERR_BLOCK_ORDER);
+      }
       joined = __ballot_sync(0xffffffffu, same);
       const int off_before = __shfl_up_sync(0xffffffffu, off, 1);
       rising = __ballot_sync(0xffffffffu, off_before + 1 == off);
@@ -416,7 +423,18 @@ __global__ void __launch_bounds__(kNormThreads, int8_write_ctas(D))
     return false;
   };
   fetch(blockIdx.x);
+  // a short call's tokens, one per thread: its blocks' second runs are found wherever they are
+  const bool all_seen = a.num_tokens <= kNormThreads;
+  const int64_t my_slot = all_seen && static_cast<int>(threadIdx.x) < a.num_tokens ? a.slot_mapping[threadIdx.x] : -1;
   if (!next_tile()) return;
+  if (all_seen) {
+    for (int i = 1; i <= 1 << a.tile_log2; ++i) {
+      const int b = __shfl_sync(0xffffffffu, block, i), end = i + __ffs(~(joined >> (i + 1))) - 1;
+      // (a run that reaches the window's end repeats slots)
+      if (b >= 0 && my_slot >> 4 == b && end < 31 && static_cast<int>(threadIdx.x) > t0 - 1 + end)
+        atomicOr(err, PHOTON_DEVERR_BLOCK_ORDER);
+    }
+  }
   for (int buf = 0;; buf ^= 1) {
     if (rotate) {
       rope_table_rows<D>(cs[buf] + (first - 1), last + 1 - first, a.turns, a.rope_style == PHOTON_ROPE_GPTJ,
