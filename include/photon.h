@@ -466,6 +466,8 @@ int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const
  *                may be NULL only when num_q_tokens is 0
  *   q_weight, k_weight  device [head_dim], kv_dtype, 16-B aligned
  *   eps          > 0, finite
+ *   q_positions, positions  any int32: padding rows, which have position -1, are
+ *                normalised and rotated like the others
  * Other arguments and errors as photon_rope_q_kv_cache_write.
  */
 int photon_qk_norm_rope_kv_cache_write(void *q, const int32_t *q_positions, int32_t num_q_tokens,
