@@ -668,39 +668,47 @@ cudaError_t launch_int8_cluster(const DecodeArgs &a, unsigned int *err, cudaStre
   constexpr int ST = 2, SMEM = Int8Ring<D, PP, ST, NW>::SMEM;
   constexpr int MIN_CTAS = PP == 1 ? 4 : 1;
   auto kern = paged_decode_int8_kernel<D, PP, ST, NW, MIN_CTAS, false, Mode::kCluster>;
-  static std::atomic<int> occupancy[64];  // per device; 0 = not set up (races repeat it)
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64) return cudaErrorInvalidDevice;
-  int occ = occupancy[dev].load(std::memory_order_relaxed);
-  if (occ == 0) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, NW * 32, SMEM);
-    if (e != cudaSuccess) return e;
-    occ = occ > 0 ? occ : 1;
-    occupancy[dev].store(occ, std::memory_order_relaxed);
-  }
-  const int64_t sms = device_sm_count(), pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  const int64_t pages = (static_cast<int64_t>(a.ctx_cap) + kBlockSize - 1) / kBlockSize;
-  int ctas = kClusterMax;  // of a cluster: all resident at once, a step's pages at least per warp
-  while (ctas > 1 && (pairs * ctas > sms * occ || ctas * NW * PP > pages)) ctas /= 2;
-  const int64_t share = (pages + ctas * NW - 1) / (ctas * NW);
-  *taken = share <= kClusterPages && (2 * pairs * ctas >= sms || share * int8_record_bytes(D) <= kClusterFewBytes + 512);
-  if (!*taken || pairs == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ctas));
   cfg.blockDim = dim3(NW * 32);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  // Clusters of 1, 2, 4 and 8 CTAs that the device holds at once, per device; 0 = not set up
+  // (races repeat it).  Fewer than its CTAs would make: a cluster lies within one GPC.
+  static std::atomic<int> resident[64][4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (resident[dev][0].load(std::memory_order_acquire) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;
+    for (int i = 3; i >= 0; --i) {  // the first entry last: it says that the others are there
+      attr[0].val.clusterDim.x = 1 << i;
+      cfg.gridDim = dim3(1 << i);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      resident[dev][i].store(std::max(n, 1), std::memory_order_release);
+    }
+  }
+  const int64_t sms = device_sm_count(), pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  const int64_t pages = (static_cast<int64_t>(a.ctx_cap) + kBlockSize - 1) / kBlockSize;
+  static_assert(kClusterMax == 8, "resident has an entry for each width");
+  int width = 3;  // of a cluster, log2: all resident at once, a step's pages at least per warp
+  while (width > 0 && (pairs > resident[dev][width].load(std::memory_order_relaxed) || (NW * PP << width) > pages)) --width;
+  const int ctas = 1 << width;
+  const int64_t share = (pages + ctas * NW - 1) / (ctas * NW);
+  *taken = share <= kClusterPages && (2 * pairs * ctas >= sms || share * int8_record_bytes(D) <= kClusterFewBytes + 512);
+  if (!*taken || pairs == 0) return cudaSuccess;
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ctas));
+  attr[0].val.clusterDim.x = ctas;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a, err);
 }

@@ -26,6 +26,11 @@ class _KernelNode(ctypes.Structure):  # CUDA_KERNEL_NODE_PARAMS
 def launches(call):
     """[(kernel's name, CTAs, threads per CTA)] of call(stream), which runs once captured
     and never replayed."""
+    return [(name, ctas, threads) for name, ctas, threads, _, _ in _captured(call)]
+
+
+def _captured(call):
+    """The same with the shared memory of a CTA and the kernel's handle."""
     torch = _torch()
     cu = ctypes.CDLL("libcuda.so.1")
 
@@ -57,7 +62,7 @@ def launches(call):
         full = subprocess.run(["c++filt", name.value.decode()], capture_output=True, text=True).stdout
         full = full.replace("photon::", "").replace("(anonymous namespace)::", "").replace("void ", "")
         found.append((full.split("(DecodeArgs")[0].split("(NormRopeArgs")[0].split("(photon")[0].strip(),
-                      int(np.prod(list(p.grid))), int(np.prod(list(p.block)))))
+                      int(np.prod(list(p.grid))), int(np.prod(list(p.block))), p.shared, p.func or p.kern))
     ok(cu.cuGraphDestroy(graph))
     return found
 
@@ -91,7 +96,7 @@ def _decode_launches(pk, B, H, G, d, max_ctx, part, out):
     bt, cl = (torch.zeros(*s, dtype=torch.int32, device="cuda") for s in ((B, W), (B,)))
     call = lambda st: pk.photon_paged_attention_decode_int8(q, pool, bt, cl, 0.1, o, max_ctx, part, ws, stream=st)
     call(None)                                                     # sets the kernels' attributes up
-    return launches(call)
+    return _captured(call)
 
 
 # Whole contexts as items, too many for clusters: one piece per row and no merge.
@@ -134,3 +139,38 @@ def test_every_launch_shape_of_the_8_bit_decode_is_tested():
                     (64, 2, 4, True, "team"), (64, 2, 4, False, "team"), (128, 2, 4, True, "team"), (128, 2, 4, False, "team"),
                     (64, 2, 12, True, "warps"), (64, 2, 4, True, "warps"), (64, 2, 4, False, "warps"), (128, 2, 8, True, "warps"),
                     (128, 2, 8, False, "warps")}
+
+
+class _Attribute(ctypes.Structure):  # CUlaunchAttribute
+    _fields_ = [("id", ctypes.c_int), ("pad", ctypes.c_int), ("dim", ctypes.c_uint * 3), ("rest", ctypes.c_char * 52)]
+
+
+class _Config(ctypes.Structure):  # CUlaunchConfig
+    _fields_ = [("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3), ("shared", ctypes.c_uint), ("stream", ctypes.c_void_p),
+                ("attrs", ctypes.POINTER(_Attribute)), ("n", ctypes.c_uint)]
+
+
+def _resident_clusters(func, size, threads, shared):
+    attr = _Attribute(id=4, dim=(size, 1, 1))                      # CU_LAUNCH_ATTRIBUTE_CLUSTER_DIMENSION
+    cfg = _Config(grid=(size, 1, 1), block=(threads, 1, 1), shared=shared, attrs=ctypes.pointer(attr), n=1)
+    n = ctypes.c_int()
+    status = ctypes.CDLL("libcuda.so.1").cuOccupancyMaxActiveClusters(ctypes.byref(n), ctypes.c_void_p(func), ctypes.byref(cfg))
+    assert status == 0, status
+    return n.value
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_clusters_of_several_ctas_are_resident_at_once(d):
+    """A second round of clusters costs a whole one: 16 pairs of sequence and KV head took 15
+    clusters of 8 CTAs and then one more."""
+    torch = _torch()
+    pk = ensure_built()
+    several = 0
+    for H in (1, 2, 8):
+        for B in list(range(1, 41)) + [75, 76, 80, 147, 152]:
+            for max_ctx in (256, 1024, 2048, 4096, 8192):
+                (name, ctas, threads, shared, func), *_ = _decode_launches(pk, B, H, 1, d, max_ctx, 64, torch.bfloat16)
+                if name.endswith("(Mode)2>") and ctas > B * H:
+                    assert B * H <= _resident_clusters(func, ctas // (B * H), threads, shared), (B, H, max_ctx)
+                    several += 1
+    assert several > 100
