@@ -461,7 +461,8 @@ int photon_paged_attention_decode_fp4(const void *q, const void *kv_cache, const
  *   N(x, w)_e    = x_e w_e / sqrt(mean_e x_e^2 + eps)
  * The mean square, the norm and the rotation are fp32, rounded once to kv_dtype:
  * before that rounding a value is within 2^-19 times its normalised pair's length of the
- * exact one.  The mean square must fit fp32 (|x| below 2^60).
+ * exact one, for eps of at least 2^-100.  The mean square and the products x_e w_e must
+ * fit fp32 (|x| below 2^60; products below 2^-126 count with a step of 2^-149).
  *   q            device [num_q_tokens][num_q_heads][head_dim], kv_dtype, 16-B aligned;
  *                may be NULL only when num_q_tokens is 0
  *   q_weight, k_weight  device [head_dim], kv_dtype, 16-B aligned

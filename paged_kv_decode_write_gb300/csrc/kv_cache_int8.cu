@@ -25,11 +25,14 @@
 // Two runs of one block in a call would race for its scale. Nothing orders them; where a
 // tile's 32 tokens, or those of a call of at most 256, show them, an error bit does.
 //
-// What bounds it: the arithmetic's issue and latency at 16 (d 64) or 8 (d 128) warps per
-// SM, not memory: 16384 tokens of 8 x 64, bf16, take 17.0 us for 50 MB (7.4 at the copy rate),
-// 13.8 without the rotation, and without either loads or stores still 12.9; 65536 tokens
-// 54.6 us, 0.54 of the copy rate; 8192 of 8 x 128 18.4 us; 64 tokens of a decode step 3.9 us,
-// two dependent loads and a launch.  The read is bound by DRAM, two thirds of it
+// What bounds it: latency at 16 (d 64) or 8 (d 128) warps per SM, whose rows fill the
+// registers, and an uneven last round of tiles; neither memory nor the issue slots (active half
+// of the time).  16384 tokens of 8 x 64, bf16, take 16.4 us for 50 MB (7.4 at the copy rate;
+// 13.4 without the rotation): 1024 tiles over 304 CTAs, so some CTAs walk four where 3.4 would do.
+// 65536 tokens, 13.5 tiles a CTA, 52.8 us, 0.56 of the copy rate; 8192 of 8 x 128 18.1 us; 64 tokens
+// of a decode step 3.9 us, two dependent loads and a launch.  Of a run's 2 x heads units a warp
+// takes whole ones: with one KV head two warps of a CTA work (16384 tokens of 1 x 64 10.2 us, 1 x 128 18.4,
+// where 4 heads take 11.3 and 20.5).  The read is bound by DRAM, two thirds of it
 // writes: 32768 tokens of 8 x 128 34.2 us, 0.87 of the copy rate.
 #include <climits>
 
@@ -562,7 +565,7 @@ cudaError_t launch_read(const CacheReadArgs &a, unsigned int *err, cudaStream_t 
 template <typename Tag, int D>
 cudaError_t launch_write(NormRopeArgs a, bool norm, unsigned int *err, cudaStream_t st) {
   // tokens per tile: as few as leave no whole tile more than there are resident CTAs, up to 16
-  // (777 fp32 tokens of 4 x 128: 5.5 us, 8.6 with a quarter of them in a tile, three tiles to a
+  // (777 fp32 tokens of 4 x 128: 5.3 us, 8.6 with a quarter of them in a tile, three tiles to a
   // CTA).  A ragged tile beyond them is walked second by one CTA; counted too, it would double
   // all tiles: 1217 tokens of 8 x 128, singles 8.2 -> 12.7 us, a prompt 6.0 -> 7.2, though 609
   // singles of 8 x 64 4.7 -> 4.3.
@@ -582,8 +585,8 @@ cudaError_t launch_write(NormRopeArgs a, bool norm, unsigned int *err, cudaStrea
 
 // Query rows from which they get a launch of their own, in the bf16 / fp32 write's
 // kernel, whose registers leave 32 warps per SM to this one's 16 (d 64) or 8 (d 128).  d 64:
-// 524288 rows, with 16384 tokens, 45.5 -> 44.0 us, 262144 24.9 against 25.7; d 128: 131072 rows,
-// with 8192 tokens, 44.7 -> 38.3, 65536 18.6 against 20.2.
+// 524288 rows, with 16384 tokens, 44.8 -> 42.9 us, 262144 24.4 against 24.5; d 128: 131072 rows,
+// with 8192 tokens, 44.1 -> 37.2, 65536 18.3 against 19.0.
 constexpr int64_t query_rows_apart(int head_dim) { return head_dim == 64 ? 524288 : 131072; }
 
 cudaError_t launch_kv_cache_write_int8(NormRopeArgs a, bool norm, photon_dtype in_dt, int head_dim,

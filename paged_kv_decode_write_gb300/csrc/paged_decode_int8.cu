@@ -28,12 +28,12 @@
 //    d 64.)  The accumulators carry 2^(14 - E) to the end of the item, the sum never.
 //    Sums, maxima and accumulators are fp32.
 //
-// What bounds it: DRAM on long steps (with the merge, 128 contexts of up to 32k tokens,
-// d 64, 2.15 GB: 329 us, 6.55 TB/s where a copy reads and writes 6.79; 64 of up to 16k, d 128, 164
-// us, 0.97 of the copy rate); between, start-up, uneven ends and the merge (64 ragged
-// sequences of d 128, 258 MB: 47.5 us, 0.80: the first page lands after 3 to 4 us, the bulk runs
-// at the copy rate, the last warp ends 4 us after the median one, the merge takes 1.5);
-// latency on short ones (one context of 1024: 4.1 us).
+// What bounds it: DRAM on long steps, the issue slots close behind (with the merge, 128
+// contexts of up to 32k tokens, d 64, 2.15 GB: 327 us, 6.58 TB/s where a copy reads and
+// writes 6.79; 64 of up to 16k, d 128, 164 us, 0.97 of the copy rate); between, start-up,
+// uneven ends and the merge (64 ragged sequences of d 128, 258 MB: 47.6 us, 0.80: the first
+// page lands after 3 to 4 us, the bulk runs at the copy rate, the last warp ends 4 us after
+// the median one, the merge takes 1.5); latency on short ones (one context of 1024: 4.1 us).
 #include <algorithm>
 #include <atomic>
 
@@ -575,17 +575,18 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
 
 // Ring depth: about 100 to 130 KB of pages on their way per SM.  That is already
 // twice what the latency needs at the memory's rate, and what lies beyond it only
-// queues, unevenly: the warps served last at the start finish last.  Shallower
-// rings against deeper ones (128 contexts of up to 32k, d 64: three stages of two
-// pages in 16 warps 354 us, two stages 335; 64 ragged sequences of d 128: two
-// stages of two pages in 12 warps 48.4 us, in 8 warps 46.8).
+// queues, unevenly: the warps served last at the start finish last.  Deeper against
+// these: d 128, two stages of two pages in 12 warps instead of 8: 64 contexts of up to 16k
+// 176 us for 164, 64 ragged sequences 48.9 for 47.5, one of 8192 12.7 for 10.8; d 64,
+// three stages instead of two in the 12 warps of long steps: 32 contexts of up to 8k
+// 30.8 us for 30.4, 128 of up to 32k 327.3 for 326.7.
 //
 // d 64, long steps: one CTA of 12 warps per SM instead of four of 4 (the warp
-// scheduler shares an SM evenly between a CTA's warps but prefers older CTAs): 335
-// -> 318 us on those 128 contexts, 0.99 of the copy rate.  Chosen when the page
+// scheduler shares an SM evenly between a CTA's warps but prefers older CTAs): 32 contexts
+// of up to 8k 33.2 -> 30.5 us, 128 of up to 32k 327.2 -> 326.8.  Chosen when the page
 // bound -- sequences x ceil(max context / 16) x KV heads -- reaches
-// kLongPagesPerWarp per warp: 32 contexts of up to 8k (72) are even at 29.5 us, 16 of
-// up to 2048 (9) lose 4 %, one of 1024 12 %.  d 128 takes one CTA of 8 warps always.
+// kLongPagesPerWarp per warp (those 32 contexts have 72): with 36, 64 contexts of up to 2048 lose
+// (20.7 -> 21.1) and 32 of up to 4096 win (20.9 -> 20.2).  d 128 takes one CTA of 8 warps always.
 constexpr int64_t kLongPagesPerWarp = 64;
 
 inline int64_t page_bound(const DecodeArgs &a) {
@@ -598,13 +599,14 @@ inline int64_t page_bound(const DecodeArgs &a) {
 // an idle GPU does not shorten them.  Teams are used where the least piece, or an
 // item without a workspace, has
 //  * 8 pages, without a workspace 4, and all items fit the GPU as CTAs at once (one
-//    context of 1024 in pieces of 8 pages, d 64 6.6 -> 5.1 us, d 128 9.2 -> 6.0;
-//    of 2 pages 4.9 -> 5.4, d 128 6.0 -> 6.4);
+//    context of 1024 in pieces of 8 pages, d 64 6.8 -> 5.1 us, d 128 9.6 -> 6.1;
+//    of 2 pages 4.9 -> 5.3, d 128 6.1 -> 6.6);
 //  * 16 pages, with more items: pieces as long as the workspace allows must leave
-//    warps idle (16 contexts of 2048 in partitions of 512, d 64 22.7 -> 11.1 us, d 128
-//    25.4 -> 19.1; 60 ragged ones of up to 1000 21.8 -> 16.6 and 32.7 -> 23.6; against
-//    it 16 of 2048 in partitions of 256 14.4 -> 15.2 and 17.3 -> 19.1), items without a
-//    workspace at most two to a CTA.  With 8 pages 16 of 2048 lose: 11.3 -> 15.2.
+//    warps idle (16 contexts of 2048 in partitions of 512, d 64 25.5 -> 11.9 us, d 128
+//    27.1 -> 19.7; 60 ragged ones of up to 1000 23.2 -> 16.5 and 32.9 -> 23.5; in partitions of 256
+//    16 of 2048 15.8 -> 15.7, but d 128 18.2 -> 19.7), items without a
+//    workspace at most two to a CTA.  With 8 pages 16 of 2048 lose: 11.7 -> 15.6.
+// (All taken with the clusters below left out, which have most of these steps.)
 constexpr int kTeamPages = 8, kTeamItemPages = 4, kTeamManyPages = 16;
 
 template <bool BAL>
@@ -653,14 +655,14 @@ cudaError_t launch_int8_kern(const DecodeArgs &a, unsigned int *err, cudaStream_
 // Short steps: a cluster of up to eight CTAs takes the whole context of a sequence
 // and KV head and merges in distributed shared memory: no pieces bounded by the
 // partition size, no partials in memory, no second launch.  (Decode and merge ->
-// cluster: one context of 1024 4.7 -> 4.0 us, d 128 6.0 -> 5.1; four of 4096 9.8 -> 7.3
-// and 11.0 -> 9.5; 16 of 2048 11.1 -> 9.6 and 17.6 -> 14.0; 64 ragged ones of up to
-// 256 10.0 -> 5.1 and 14.6 -> 7.8, of up to 1024 14.3 -> 11.7 and 21.7 -> 20.3; 300 of up to 700
-// 36.2 -> 27.8 and 52.6 -> 43.2.)  What it costs is evenness: a warp's share follows the longest
+// cluster: one context of 1024 4.9 -> 4.1 us, d 128 6.2 -> 5.2; four of 4096 9.5 -> 7.6
+// and 13.1 -> 10.0; 16 of 2048 11.7 -> 10.1 and 18.4 -> 14.7; 64 ragged ones of up to
+// 256 11.6 -> 5.4 and 14.9 -> 8.2, of up to 1024 15.1 -> 13.0 and 22.4 -> 21.7; 300 of up to 700
+// 37.9 -> 29.4 and 54.8 -> 45.0.)  What it costs is evenness: a warp's share follows the longest
 // context.  So it is taken while no warp has more than kClusterPages pages at the
-// declared longest one (16 ragged contexts of up to 4096, d 64, 16 pages: 13.7 against
-// 13.5), and, where the clusters leave more than half of the SMs idle, than 16 KB (8 of
-// up to 16384, 16 pages: 10.5 against 9.3; one of 8192, d 128, 8 pages: 9.4 against 8.4).
+// declared longest one (16 ragged contexts of up to 4096, d 64, 16 pages, partitions of 128:
+// 15.0 against 14.2; 8 of up to 16384, 32 pages: 24.6 against 21.8), and, where the clusters leave
+// more than half of the SMs idle, than 16 KB (one of 8192, d 128, 8 pages: 9.9 against 9.3).
 constexpr int kClusterMax = 8, kClusterPages = 16, kClusterFewBytes = 16384;
 
 template <int D, int PP, int NW>

@@ -11,10 +11,15 @@
 // contiguous, so a warp's loads are whole lines, and no warp waits for another.
 //
 // What bounds it: loads in flight, so warps per SM.  8192 tokens with 32 query and 8
-// KV heads of 64, bf16, 101 MB: 18.7 us, 0.79 of the copy rate (65536 tokens 130 us, 0.91;
-// 64 tokens of 16 / 8 heads of 128 2.1 us, latency).  With one table and a barrier for a CTA's 8
+// KV heads of 64, bf16, 101 MB: 18.4 us, 0.81 of the copy rate (65536 tokens 128 us, 0.93;
+// 64 tokens of 16 / 8 heads of 128 2.3 us, latency).  The bf16 kernels of d 32, 64 and 128 hold 64
+// registers and spill 16 bytes for those 32 warps per SM.  With one table and a barrier for a CTA's 8
 // tokens 19.5; the table row in registers, 24 warps per SM instead of 32, 19.9; two rows
-// ahead 20.1; 40 warps, whose registers spill, 25.9.
+// ahead 20.1; 40 warps, which spill more, 25.9.
+// Of middle-sized chunks with few heads most warps have no work: a token is split over up to
+// 8 warps whatever its heads, and lanes past the last head repeat it (777 fp32 tokens of 4 / 4
+// heads of 128 5.0 us for a floor of 1.4, 9 % of the warps active; 16384 tokens of 2 / 1 heads of 64
+// 15.0 us, of 8 / 4 17.1).
 #include "norm_rope.cuh"
 
 namespace photon {
