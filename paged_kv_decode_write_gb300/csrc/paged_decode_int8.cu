@@ -399,19 +399,20 @@ __global__ void __launch_bounds__(NW * 32, MIN_CTAS)
             const uint4 v0 = *reinterpret_cast<const uint4 *>(vp);        // tokens 4c, 4c + 1
             const uint4 v1 = *reinterpret_cast<const uint4 *>(vp + 512);  // tokens 4c + 2, 4c + 3
             // the four weights' MMAs, then the four remainders': none waits for the one before
-            uint32_t w[4][4];
+            uint32_t code[4][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const uint32_t x0 = t < 2 ? v0.x : v0.y, y0 = t < 2 ? v0.z : v0.w;
               const uint32_t x1 = t < 2 ? v1.x : v1.y, y1 = t < 2 ? v1.z : v1.w;
-              w[t][0] = t & 1 ? codes_across<2>(x0, y0) : codes_across<0>(x0, y0);
-              w[t][1] = t & 1 ? codes_across<3>(x0, y0) : codes_across<1>(x0, y0);
-              w[t][2] = t & 1 ? codes_across<2>(x1, y1) : codes_across<0>(x1, y1);
-              w[t][3] = t & 1 ? codes_across<3>(x1, y1) : codes_across<1>(x1, y1);
-              mma_f16(o[hh][t], w[t][0], w[t][1], w[t][2], w[t][3], ph[i][0], ph[i][1]);
+              code[t][0] = t & 1 ? codes_across<2>(x0, y0) : codes_across<0>(x0, y0);
+              code[t][1] = t & 1 ? codes_across<3>(x0, y0) : codes_across<1>(x0, y0);
+              code[t][2] = t & 1 ? codes_across<2>(x1, y1) : codes_across<0>(x1, y1);
+              code[t][3] = t & 1 ? codes_across<3>(x1, y1) : codes_across<1>(x1, y1);
+              mma_f16(o[hh][t], code[t][0], code[t][1], code[t][2], code[t][3], ph[i][0], ph[i][1]);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) mma_f16(o[hh][t], w[t][0], w[t][1], w[t][2], w[t][3], pl[i][0], pl[i][1]);
+            for (int t = 0; t < 4; ++t)
+              mma_f16(o[hh][t], code[t][0], code[t][1], code[t][2], code[t][3], pl[i][0], pl[i][1]);
           }
       }
       __syncwarp();  // the stage is read before the next copies overwrite it
